@@ -1,7 +1,8 @@
 /*
  * evo_attn.h — C ABI of the B200 (sm_100a) biased-attention library,
- * libevoattn.so: the forward pass, its backward pass, and the
- * triangle-multiplication contraction.
+ * libevoattn.so: the forward pass, its backward pass, the
+ * triangle-multiplication contraction, the gated transition and the learned
+ * relative-position bias (each with its gradients).
  *
  * The operation is the forward pass that the DeepSpeed DS4Sci_EvoformerAttention
  * guide (hmyw.cn) describes for the four Evoformer attention variants (its
@@ -328,6 +329,149 @@ EVO_API int64_t evo_trimul_workspace_size(int64_t Bt, int64_t N, int64_t C);
  */
 EVO_API int evo_trimul(const void* A, const void* B, void* Z, void* workspace, int64_t workspace_bytes,
                int64_t Bt, int64_t N, int64_t C, int outgoing, int dtype, evo_stream_t stream);
+
+/*
+ * The gated feed-forward block of these models (the "transition" that follows
+ * the triangle operations and the MSA attention in a block, on a pair, MSA or
+ * single representation), with its gradients.  The pages this library follows
+ * name the blocks but print no formula; the reading is the gated unit
+ *
+ *     G = X Wg^T,   U = X Wu^T,   H = act(G) * U,   Y = H Wd^T
+ *
+ * without bias terms, act one of evo_act_t.
+ */
+typedef enum {
+    EVO_ACT_SILU = 0,     /* g / (1 + exp(-g))                              */
+    EVO_ACT_GELU = 1      /* g Phi(g), Phi the normal distribution (erf form) */
+} evo_act_t;
+
+/*
+ * evo_transition_fwd_workspace_size, evo_transition_bwd_workspace_size —
+ * bytes of device workspace that the two calls below need for these sizes, or
+ * a negative evo_status_t for negative sizes (EVO_ERR_INVALID_ARG), another
+ * dtype (EVO_ERR_UNSUPPORTED_DTYPE) or sizes outside the envelope
+ * (EVO_ERR_UNSUPPORTED_SHAPE).
+ */
+EVO_API int64_t evo_transition_fwd_workspace_size(int64_t M, int64_t C, int64_t F, int dtype);
+EVO_API int64_t evo_transition_bwd_workspace_size(int64_t M, int64_t C, int64_t F, int dtype);
+
+/*
+ * evo_transition_fwd — the block on M rows.
+ *
+ *   X          [M, C] of `dtype`: every (b, i, j) edge, (b, n, s) MSA entry or
+ *              token is a row.
+ *   Wg, Wu     [F, C] of `dtype` (the layout of a linear layer's weight).
+ *   Wd         [C, F] of `dtype`.
+ *   Y          [M, C] of `dtype`, written.
+ *   workspace  device scratch of at least evo_transition_fwd_workspace_size
+ *              bytes, 256-byte aligned, owned by the caller, overwritten; two
+ *              calls (or captured graphs) that may run at the same time need
+ *              one each.
+ *   M, C, F    >= 0.  No row or no channel is a no-op, no feature (F = 0) gives
+ *              Y = 0.
+ *   act        an evo_act_t.  dtype: an evo_dtype_t.
+ *
+ * Arithmetic: every product is accumulated in fp32 and the activation is
+ * computed in fp32.  With bf16 and fp16, H is rounded to the type before the
+ * last product (its tensor-core operand), except in the form for a few rows,
+ * which keeps it in fp32; with fp16 an |H| past 65504 is infinite.  Y is
+ * rounded once.  The same call gives the same bits every time.
+ *
+ * Supported envelope: M < 2^31, C and F <= 2^20.  16-bit tensors 16-byte
+ * aligned when C and F are multiples of 8, else 2-byte aligned; fp32 tensors
+ * 4-byte aligned.  Y and the workspace must not overlap each other or any input.
+ * Returns EVO_OK once the work is enqueued, or a negative evo_status_t
+ * (EVO_ERR_INVALID_ARG also for a workspace that is too small).
+ */
+EVO_API int evo_transition_fwd(const void* X, const void* Wg, const void* Wu, const void* Wd, void* Y,
+                 void* workspace, int64_t workspace_bytes, int64_t M, int64_t C, int64_t F,
+                 int act, int dtype, evo_stream_t stream);
+
+/*
+ * evo_transition_bwd — gradients of a loss with respect to the inputs of
+ * evo_transition_fwd, given the gradient dY with respect to Y:
+ *
+ *     dH = dY Wd,   dG = dH * U * act'(G),   dU = dH * act(G)
+ *     dX = dG Wg + dU Wu,   dWg = dG^T X,   dWu = dU^T X,   dWd = dY^T H
+ *
+ *   X, Wg, Wu, Wd, M, C, F, act, dtype   as passed to evo_transition_fwd; G, U
+ *              and H are recomputed from them, nothing of the forward is kept.
+ *   dY         [M, C] of `dtype`.
+ *   dX         [M, C] of `dtype`, written, or NULL to skip this gradient.
+ *   dWg, dWu   [F, C], dWd [C, F] of `dtype`, each written or NULL to skip it.
+ *              With no row (M = 0) they are zero.
+ *   workspace  as above, evo_transition_bwd_workspace_size bytes.
+ *
+ * Every product and sum is held in fp32; with bf16 and fp16, H, dG and dU are
+ * rounded to the type as operands of the next products; the gradients are
+ * rounded once.  No atomic additions: the same call gives the same bits every
+ * time.  Envelope, alignment, overlap and status codes as above.
+ */
+EVO_API int evo_transition_bwd(const void* X, const void* Wg, const void* Wu, const void* Wd, const void* dY,
+                 void* dX, void* dWg, void* dWu, void* dWd,
+                 void* workspace, int64_t workspace_bytes, int64_t M, int64_t C, int64_t F,
+                 int act, int dtype, evo_stream_t stream);
+
+/*
+ * evo_relpos_fwd — the learned relative-position bias: a pair bias for
+ * evo_attn_fwd looked up by the bucket of the residue distance.
+ *
+ *     r(b,i,j)       = the number of borders <= pos_q[b,i] - pos_k[b,j],
+ *                      or num_borders + 1 where chain_q[b,i] != chain_k[b,j]
+ *     pair[b,0,h,i,j] = table[r(b,i,j), h] (+ base[b,0,h,i,j])
+ *
+ *   table      [R, H] of `dtype`: one row for each bucket, R = num_borders + 1,
+ *              one more with chains.
+ *   borders    [num_borders] int32, ascending, each above -2^31.  Bucket 0 is
+ *              everything below the first border.  (Clipped distances -r .. r:
+ *              the borders -r .. r.  Log-spaced buckets: their lower ends.)
+ *              Borders that do not ascend give an unspecified row, in bounds.
+ *   pos_q      [B, Sq] int32, pos_k [B, Sk] int32: residue numbers in any order,
+ *              repeated or with gaps; a difference past the 32-bit range counts
+ *              as the end of that range.
+ *   chain_q    [B, Sq], chain_k [B, Sk] int32, or both NULL for one chain.
+ *   base       [B, 1, H, Sq, Sk] of `dtype`, or NULL: a bias added in fp32.
+ *   pair       [B, 1, H, Sq, Sk] of `dtype`, written; without a base the exact
+ *              table values.
+ *   B, Sq, Sk, H   >= 0 (a zero size is a no-op that returns EVO_OK).  Sq = Sk = S
+ *              gives evo_attn_fwd's pair_bias; a strip of rows may be made alone.
+ *
+ * Supported envelope: num_borders <= 2048; B and H <= 65535; pointers aligned
+ * to the element size.  pair must not overlap any input.  Returns EVO_OK once
+ * enqueued, or a negative evo_status_t.
+ */
+EVO_API int evo_relpos_fwd(const void* table, const int32_t* borders, const int32_t* pos_q, const int32_t* pos_k,
+                 const int32_t* chain_q, const int32_t* chain_k, const void* base, void* pair,
+                 int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t num_borders, int dtype, evo_stream_t stream);
+
+/*
+ * evo_relpos_bwd_workspace_size — bytes of device workspace evo_relpos_bwd
+ * needs, or a negative evo_status_t as above.
+ */
+EVO_API int64_t evo_relpos_bwd_workspace_size(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t num_borders,
+                 int has_chain);
+
+/*
+ * evo_relpos_bwd — the gradient of the table, given the gradient of the pair
+ * bias (evo_attn_bwd's dpair; the gradient of `base` is dpair itself):
+ *
+ *     dtable[r, h] = sum of dpair[b,0,h,i,j] over the (b,i,j) with r(b,i,j) = r
+ *
+ *   dpair      [B, 1, H, Sq, Sk] of `dtype`.
+ *   borders, pos_q, pos_k, chain_q, chain_k, sizes, dtype   as for evo_relpos_fwd.
+ *   dtable     [R, H] of `dtype`, written: every row, zero where no pair falls
+ *              (all of it when B, Sq or Sk is zero).
+ *   workspace  device scratch of at least evo_relpos_bwd_workspace_size bytes,
+ *              256-byte aligned, owned by the caller, overwritten.
+ *
+ * Sums are held in fp32 in a fixed order (no atomics): the same call gives the
+ * same bits every time.  Also needs B * H * ceil(R / 256) <= 65535.  dtable and
+ * the workspace must not overlap each other or any input.
+ */
+EVO_API int evo_relpos_bwd(const void* dpair, const int32_t* borders, const int32_t* pos_q, const int32_t* pos_k,
+                 const int32_t* chain_q, const int32_t* chain_k, void* dtable,
+                 void* workspace, int64_t workspace_bytes,
+                 int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t num_borders, int dtype, evo_stream_t stream);
 
 /*
  * evo_attn_sync_status — synchronise `stream`, then return and clear the

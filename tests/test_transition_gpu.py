@@ -1,0 +1,200 @@
+"""The gated transition on the GPU against the float64 oracle, element by element
+within the error that fp32 accumulation and the documented roundings can cause
+(oracle/transition.py derives it)."""
+import numpy as np
+import pytest
+import torch
+
+import triangle_biased_attention_b200 as evo
+from oracle import transition as T
+
+pytestmark = pytest.mark.gpu
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def make(M, C, F, dt, seed, dev="cuda:0"):
+    gen = torch.Generator().manual_seed(seed)
+    n = lambda *s, k=1.0: (torch.randn(*s, generator=gen) * k).to(dt).to(dev)  # noqa: E731
+    return n(M, C), n(F, C, k=C ** -0.5), n(F, C, k=C ** -0.5), n(C, F, k=F ** -0.5), n(M, C)
+
+
+def within(got, ref, err, what):
+    got = T._f64(got)
+    assert got.shape == ref.shape and np.isfinite(got).all(), what
+    ratio = float((np.abs(got - ref) / err).max(initial=0))
+    print(f"{what}: max err/bound {ratio:.3f}")
+    assert ratio <= 1.0, what
+
+
+def check(x, wg, wu, wd, dy, act, what, stream=None):
+    dt = x.dtype
+    y = evo.transition(x, wg, wu, wd, act=act, stream=stream)
+    grads = evo.transition_backward(x, wg, wu, wd, dy, act=act, stream=stream)
+    assert evo.evo_attn_sync_status(None if stream is None else stream.cuda_stream) == evo.EVO_OK
+    torch.cuda.synchronize()
+    ref, err = T.forward(x, wg, wu, wd, act, dt)
+    within(y, ref, err, f"{what} y")
+    ref, err = T.backward(x, wg, wu, wd, dy, act, dt)
+    for name, g, r, e in zip(("dx", "dw_gate", "dw_up", "dw_down"), grads, ref, err):
+        within(g, r, e, f"{what} {name}")
+
+
+SHAPES = [
+    # M, C, F: one token to several row tiles; whole tiles, ragged ones, odd channels and features
+    (1, 1, 1), (1, 384, 1536), (2, 64, 256), (3, 40, 72), (5, 7, 9), (8, 128, 512), (9, 128, 512), (17, 33, 130),
+    (127, 128, 128), (128, 64, 64), (129, 136, 264), (300, 256, 512), (257, 100, 397), (1000, 16, 24), (640, 384, 640),
+]
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32], ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_matches_oracle(shape, dt):
+    M, C, F = shape
+    act = "gelu" if (M + C + F) % 2 else "silu"
+    check(*make(M, C, F, dt, seed=M + C + F), act, f"{shape} {dt} {act}")
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32], ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_both_activations(act, dt):
+    check(*make(200, 96, 160, dt, seed=5), act, f"{act} {dt}")
+
+
+def test_more_rows_than_one_chunk():
+    """Rows are taken in chunks; the weight gradients add up over them."""
+    M, C, F = 2 * 18944 + 300, 16, 1200
+    assert evo.evo_transition_bwd_workspace_size(M, C, F, evo.EVO_DTYPE_BF16) == \
+        evo.evo_transition_bwd_workspace_size(M + 18944, C, F, evo.EVO_DTYPE_BF16)
+    check(*make(M, C, F, BF16, seed=1), "silu", f"chunks {M}")
+
+
+def test_activation_range():
+    """Gates far out on both sides: no overflow on the way to 0 or to g."""
+    gates = torch.tensor([-1e30, -3e4, -100.0, -88.5, -87.0, -20.0, -1.0, -0.0, 1e-30, 20.0, 100.0, 1e3])
+    for dt in (BF16, FP32):
+        x = torch.zeros(12, 16)
+        x[:, 0], x[:, 1] = gates, 1.0
+        wg, wu, wd = torch.zeros(16, 16), torch.zeros(16, 16), torch.eye(16)
+        wg[:, 0], wu[:, 1] = 1.0, 1.0
+        x, wg, wu, wd = (t.to(dt).cuda() for t in (x, wg, wu, wd))
+        for act in ("silu", "gelu"):
+            y = evo.transition(x, wg, wu, wd, act=act)
+            ref, err = T.forward(x, wg, wu, wd, act, dt)
+            # far tails come out below the type's normal numbers
+            assert np.all(np.abs(T._f64(y) - ref) <= err + 2.0 ** -100), (dt, act)
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_nan_stays_in_its_row(M):
+    x, wg, wu, wd, _ = make(M + 1, 64, 128, BF16, seed=2)
+    clean = evo.transition(x, wg, wu, wd)
+    x[M, 3] = float("nan")
+    y = evo.transition(x, wg, wu, wd)
+    assert torch.isnan(y[M]).all() and torch.equal(y[:M], clean[:M])
+
+
+def test_empty_sizes():
+    x, wg, wu, wd, dy = make(4, 16, 24, BF16, seed=0)
+    assert evo.transition(x[:0], wg, wu, wd).shape == (0, 16)
+    dx, *dw = evo.transition_backward(x[:0], wg, wu, wd, dy[:0])
+    assert dx.shape == (0, 16) and all((g == 0).all() for g in dw)
+    none = torch.empty(0, 16, dtype=BF16, device="cuda")
+    y = evo.transition(x, none, none, none.T.contiguous(), out=torch.full_like(x, 7))
+    assert (y == 0).all()
+    dx, *_ = evo.transition_backward(x, none, none, none.T.contiguous(), dy)
+    assert (dx == 0).all()
+
+
+def test_only_the_asked_gradients():
+    x, wg, wu, wd, dy = make(300, 64, 96, BF16, seed=4)
+    full = evo.transition_backward(x, wg, wu, wd, dy)
+    dx, *none = evo.transition_backward(x, wg, wu, wd, dy, need_dw=False)
+    assert none == [None] * 3 and torch.equal(dx, full[0])
+    none, *dw = evo.transition_backward(x, wg, wu, wd, dy, need_dx=False)
+    assert none is None and all(torch.equal(a, b) for a, b in zip(dw, full[1:]))
+    # one weight's gradient alone, through the C entry point
+    M, C, F = 300, 64, 96
+    ws = torch.empty(evo.evo_transition_bwd_workspace_size(M, C, F, 0), dtype=torch.uint8, device="cuda")
+    for i in range(3):
+        out = [None] * 3
+        out[i] = torch.full_like((wg, wu, wd)[i], 9)
+        st = evo.evo_transition_bwd(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), wd.data_ptr(), dy.data_ptr(), None,
+                                    *(None if o is None else o.data_ptr() for o in out), ws.data_ptr(), ws.numel(), M, C,
+                                    F, 0, evo.EVO_DTYPE_BF16, None)
+        torch.cuda.synchronize()
+        assert st == evo.EVO_OK and torch.equal(out[i], full[1 + i])
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=lambda d: str(d)[6:])
+@pytest.mark.parametrize("shape", [(4, 64, 128), (700, 72, 200)], ids=str)
+def test_same_bits_every_time_and_writes_only_its_rows(shape, dt):
+    M, C, F = shape
+    x, wg, wu, wd, dy = make(M, C, F, dt, seed=6)
+    out = torch.full((M + 3, C), 5.0, dtype=dt, device="cuda")
+    y = evo.transition(x, wg, wu, wd, out=out[:M])
+    assert (out[M:] == 5).all()
+    g = evo.transition_backward(x, wg, wu, wd, dy)
+    for _ in range(3):
+        assert torch.equal(evo.transition(x, wg, wu, wd), y)
+        assert all(torch.equal(a, b) for a, b in zip(evo.transition_backward(x, wg, wu, wd, dy), g))
+
+
+def test_leading_axes_are_rows():
+    x, wg, wu, wd, dy = make(24, 32, 64, FP16, seed=7)
+    y = evo.transition(x, wg, wu, wd)
+    assert torch.equal(evo.transition(x.view(2, 3, 4, 32), wg, wu, wd), y.view(2, 3, 4, 32))
+    assert torch.equal(evo.transition(x[0], wg, wu, wd), evo.transition(x[:1], wg, wu, wd)[0])
+    dx, *_ = evo.transition_backward(x.view(2, 12, 32), wg, wu, wd, dy.view(2, 12, 32))
+    assert dx.shape == (2, 12, 32)
+
+
+def test_unaligned_tensors():
+    """2-byte aligned tensors run where C or F is no multiple of 8, and are refused elsewhere."""
+    def shifted(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+        buf[1:] = t.flatten()
+        return buf[1:].view(t.shape)
+    check(*(shifted(t) for t in make(140, 50, 70, BF16, seed=8)), "silu", "unaligned")
+    check(*(shifted(t) for t in make(140, 48, 64, FP32, seed=8)), "silu", "unaligned fp32")
+    check(*(shifted(t) for t in make(3, 50, 70, BF16, seed=8)), "silu", "unaligned, few rows")
+    x, wg, wu, wd, _ = make(140, 48, 64, BF16, seed=8)
+    with pytest.raises(evo.EvoAttnError) as e:
+        evo.transition(shifted(x), wg, wu, wd)
+    assert e.value.status == evo.EVO_ERR_MISALIGNED
+
+
+def test_another_stream_and_two_calls_at_once():
+    side = torch.cuda.Stream()
+    a, b = make(600, 128, 256, BF16, seed=9), make(600, 128, 256, BF16, seed=10)
+    torch.cuda.synchronize()
+    check(*a, "silu", "side stream", stream=side)
+    wants = [evo.transition(*t[:4]) for t in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        y0 = evo.transition(*a[:4], stream=side)
+        y1 = evo.transition(*b[:4])
+        torch.cuda.synchronize()
+        assert torch.equal(y0, wants[0]) and torch.equal(y1, wants[1])
+
+
+@pytest.mark.parametrize("shape,dt", [((1, 384, 512), BF16), ((500, 64, 96), BF16), ((500, 50, 70), FP16),
+                                      ((130, 32, 48), FP32)], ids=str)
+def test_replays_in_a_cuda_graph(shape, dt):
+    M, C, F = shape
+    first, second = make(M, C, F, dt, seed=11), make(M, C, F, dt, seed=12)
+    bufs = [t.clone() for t in first]
+    evo.transition(*bufs[:4])
+    evo.transition_backward(*bufs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = evo.transition(*bufs[:4])
+        grads = evo.transition_backward(*bufs)
+    for case in (second, first):
+        for buf, t in zip(bufs, case):
+            buf.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert evo.evo_attn_sync_status() == evo.EVO_OK
+        assert torch.equal(y, evo.transition(*case[:4]))
+        assert all(torch.equal(a, b) for a, b in zip(grads, evo.transition_backward(*case)))

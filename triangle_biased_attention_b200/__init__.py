@@ -11,11 +11,15 @@ pair_bias [B, 1, H, S, S] (shared by every n), and its backward pass (the
 gradients of Q, K, V and of the biases, sections 1 and 5.4).  All arithmetic runs in the
 CUDA library ``libevoattn.so`` (hand-written sm_100a kernels behind the C ABI
 in ``include/evo_attn.h``); this module only marshals arguments through
-ctypes.  PyTorch supplies device memory and the current stream.  There is no
+ctypes.  Around the attention the library has triangle multiplication
+(``trimul``), the gated transition (``transition``) and the learned
+relative-position bias that serves as a pair bias (``relpos_bias``), the last
+two with their gradients.  PyTorch supplies device memory and the current stream.  There is no
 fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -30,11 +34,18 @@ __all__ = [
     "EVO_OK", "EVO_ERR_INVALID_ARG", "EVO_ERR_UNSUPPORTED_DTYPE", "EVO_ERR_UNSUPPORTED_SHAPE",
     "EVO_ERR_MISALIGNED", "EVO_ERR_CUDA", "EVO_ERR_TIMEOUT", "EVO_ERR_RANGE", "EVO_ERR_SCRATCH",
     "evo_attn_bwd_noalloc", "NOALLOC_SCRATCH_BYTES", "evo_trimul", "evo_trimul_workspace_size", "trimul",
+    "EVO_ACT_SILU", "EVO_ACT_GELU", "evo_transition_fwd", "evo_transition_bwd", "evo_transition_fwd_workspace_size",
+    "evo_transition_bwd_workspace_size", "transition", "transition_backward",
+    "evo_relpos_fwd", "evo_relpos_bwd", "evo_relpos_bwd_workspace_size", "relpos_bias", "relpos_bias_backward",
+    "relpos_clip_borders", "relpos_log_borders",
 ]
 
 EVO_DTYPE_BF16 = 0
 EVO_DTYPE_FP32 = 1
 EVO_DTYPE_FP16 = 2
+
+EVO_ACT_SILU = 0
+EVO_ACT_GELU = 1
 
 EVO_OK = 0
 EVO_ERR_INVALID_ARG = -1
@@ -53,6 +64,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libevoattn.so")
 _lib = None
 
+_ACTS = {"silu": EVO_ACT_SILU, "gelu": EVO_ACT_GELU}
 _DTYPES = {torch.bfloat16: EVO_DTYPE_BF16, torch.float32: EVO_DTYPE_FP32, torch.float16: EVO_DTYPE_FP16}
 
 
@@ -99,6 +111,20 @@ def load_library():
     lib.evo_trimul_workspace_size.restype = i64
     lib.evo_trimul.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, vp]
     lib.evo_trimul.restype = i32
+    lib.evo_transition_fwd_workspace_size.argtypes = [i64, i64, i64, i32]
+    lib.evo_transition_fwd_workspace_size.restype = i64
+    lib.evo_transition_bwd_workspace_size.argtypes = [i64, i64, i64, i32]
+    lib.evo_transition_bwd_workspace_size.restype = i64
+    lib.evo_transition_fwd.argtypes = [vp] * 6 + [i64, i64, i64, i64, i32, i32, vp]
+    lib.evo_transition_fwd.restype = i32
+    lib.evo_transition_bwd.argtypes = [vp] * 10 + [i64, i64, i64, i64, i32, i32, vp]
+    lib.evo_transition_bwd.restype = i32
+    lib.evo_relpos_fwd.argtypes = [vp] * 8 + [i64, i64, i64, i64, i64, i32, vp]
+    lib.evo_relpos_fwd.restype = i32
+    lib.evo_relpos_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, i32]
+    lib.evo_relpos_bwd_workspace_size.restype = i64
+    lib.evo_relpos_bwd.argtypes = [vp] * 8 + [i64, i64, i64, i64, i64, i64, i32, vp]
+    lib.evo_relpos_bwd.restype = i32
     _lib = lib
     return lib
 
@@ -164,6 +190,49 @@ def evo_trimul(A, B, Z, workspace, workspace_bytes: int, Bt: int, N: int, C: int
                stream: Optional[int]) -> int:
     """The C triangle-multiplication entry point with raw addresses; returns the status code."""
     return int(load_library().evo_trimul(A, B, Z, workspace, workspace_bytes, Bt, N, C, outgoing, dtype, stream))
+
+
+def evo_transition_fwd_workspace_size(M: int, C: int, F: int, dtype: int) -> int:
+    """Workspace bytes of evo_transition_fwd, or a negative status code."""
+    return int(load_library().evo_transition_fwd_workspace_size(M, C, F, dtype))
+
+
+def evo_transition_bwd_workspace_size(M: int, C: int, F: int, dtype: int) -> int:
+    """Workspace bytes of evo_transition_bwd, or a negative status code."""
+    return int(load_library().evo_transition_bwd_workspace_size(M, C, F, dtype))
+
+
+def evo_transition_fwd(X, Wg, Wu, Wd, Y, workspace, workspace_bytes: int, M: int, C: int, F: int, act: int,
+                       dtype: int, stream: Optional[int]) -> int:
+    """The C transition entry point with raw addresses; returns the status code."""
+    return int(load_library().evo_transition_fwd(X, Wg, Wu, Wd, Y, workspace, workspace_bytes, M, C, F, act, dtype,
+                                                 stream))
+
+
+def evo_transition_bwd(X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, workspace, workspace_bytes: int, M: int, C: int, F: int,
+                       act: int, dtype: int, stream: Optional[int]) -> int:
+    """The C transition backward entry point with raw addresses; returns the status code."""
+    return int(load_library().evo_transition_bwd(X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, workspace, workspace_bytes,
+                                                 M, C, F, act, dtype, stream))
+
+
+def evo_relpos_fwd(table, borders, pos_q, pos_k, chain_q, chain_k, base, pair, B: int, Sq: int, Sk: int, H: int,
+                   num_borders: int, dtype: int, stream: Optional[int]) -> int:
+    """The C relative-position entry point with raw addresses; returns the status code."""
+    return int(load_library().evo_relpos_fwd(table, borders, pos_q, pos_k, chain_q, chain_k, base, pair, B, Sq, Sk, H,
+                                             num_borders, dtype, stream))
+
+
+def evo_relpos_bwd_workspace_size(B: int, Sq: int, Sk: int, H: int, num_borders: int, has_chain: int) -> int:
+    """Workspace bytes of evo_relpos_bwd, or a negative status code."""
+    return int(load_library().evo_relpos_bwd_workspace_size(B, Sq, Sk, H, num_borders, has_chain))
+
+
+def evo_relpos_bwd(dpair, borders, pos_q, pos_k, chain_q, chain_k, dtable, workspace, workspace_bytes: int, B: int,
+                   Sq: int, Sk: int, H: int, num_borders: int, dtype: int, stream: Optional[int]) -> int:
+    """The C relative-position backward entry point with raw addresses; returns the status code."""
+    return int(load_library().evo_relpos_bwd(dpair, borders, pos_q, pos_k, chain_q, chain_k, dtable, workspace,
+                                             workspace_bytes, B, Sq, Sk, H, num_borders, dtype, stream))
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -378,3 +447,239 @@ def trimul(a: torch.Tensor, b: torch.Tensor, outgoing: bool = True, out: Optiona
     if status != EVO_OK:
         raise EvoAttnError(status, "evo_trimul")
     return out
+
+
+def _same(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _call_stream(stream: Optional[torch.cuda.Stream], device):
+    """The stream of a call and a context in which its outputs and workspace are
+    allocated, so that they belong to that stream."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        return torch.cuda.current_stream(device), contextlib.nullcontext()
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return stream, torch.cuda.stream(stream)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device, what: str) -> torch.Tensor:
+    if need < 0:
+        raise EvoAttnError(need, what)
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _transition_args(x, w_gate, w_up, w_down, act):
+    if x.dim() < 1:
+        raise ValueError("x must be [..., C]")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    C = x.shape[-1]
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate must be [F, C]")
+    F = w_gate.shape[0]
+    for name, t, shape in (("w_gate", w_gate, (F, C)), ("w_up", w_up, (F, C)), ("w_down", w_down, (C, F))):
+        _same(name, t, shape, x.dtype, x.device)
+    M = 1
+    for n in x.shape[:-1]:
+        M *= n
+    return M, C, F
+
+
+def transition(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, act: str = "silu",
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gated feed-forward block on CUDA tensors; returns Y [..., C] =
+    (act(x w_gate^T) * (x w_up^T)) w_down^T.
+
+    x: [..., C] bf16, fp16 or fp32, contiguous (a pair, MSA or single
+    representation, or one token).  w_gate, w_up: [F, C]; w_down: [C, F], x's
+    dtype.  act: "silu" or "gelu" (erf form).  ``workspace``: optional uint8 CUDA
+    tensor of ``evo_transition_fwd_workspace_size`` bytes (allocated here when
+    not given; calls that may run at the same time need one each).  Runs on
+    ``stream`` (default: the current stream) without synchronising.
+    """
+    M, C, F = _transition_args(x, w_gate, w_up, w_down, act)
+    stream, scope = _call_stream(stream, x.device)
+    code = _DTYPES[x.dtype]
+    with scope:
+        if out is None:
+            out = torch.empty_like(x)
+        else:
+            _same("out", out, x.shape, x.dtype, x.device)
+        workspace = _workspace(workspace, evo_transition_fwd_workspace_size(M, C, F, code), x.device,
+                               "evo_transition_fwd_workspace_size")
+    status = evo_transition_fwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), out.data_ptr(),
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), M, C, F, _ACTS[act],
+                                code, stream.cuda_stream)
+    if status != EVO_OK:
+        raise EvoAttnError(status, "evo_transition_fwd")
+    return out
+
+
+def transition_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                        dy: torch.Tensor, act: str = "silu", need_dx: bool = True, need_dw: bool = True,
+                        workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of ``transition`` for the upstream gradient dy ([..., C], x's
+    dtype); returns (dx, dw_gate, dw_up, dw_down).
+
+    The other arguments are the forward's; nothing else of the forward is kept.
+    dx is None without ``need_dx``, the three weight gradients are None without
+    ``need_dw``.  ``workspace``: optional uint8 CUDA tensor of
+    ``evo_transition_bwd_workspace_size`` bytes.  Runs on ``stream`` (default: the
+    current stream) without synchronising.
+    """
+    M, C, F = _transition_args(x, w_gate, w_up, w_down, act)
+    _same("dy", dy, x.shape, x.dtype, x.device)
+    stream, scope = _call_stream(stream, x.device)
+    code = _DTYPES[x.dtype]
+    with scope:
+        dx = torch.empty_like(x) if need_dx else None
+        dw = [torch.empty_like(w) for w in (w_gate, w_up, w_down)] if need_dw else [None] * 3
+        workspace = _workspace(workspace, evo_transition_bwd_workspace_size(M, C, F, code), x.device,
+                               "evo_transition_bwd_workspace_size")
+    status = evo_transition_bwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), dy.data_ptr(),
+                                _ptr(dx), _ptr(dw[0]), _ptr(dw[1]), _ptr(dw[2]), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), M, C, F, _ACTS[act], code,
+                                stream.cuda_stream)
+    if status != EVO_OK:
+        raise EvoAttnError(status, "evo_transition_bwd")
+    return dx, dw[0], dw[1], dw[2]
+
+
+def relpos_clip_borders(radius: int) -> torch.Tensor:
+    """Borders of one bucket for each distance -radius .. radius - 1, one for
+    everything below and one for radius and beyond: int32 [2 radius + 1] on the CPU."""
+    if radius < 0:
+        raise ValueError("radius must be >= 0")
+    return torch.arange(-radius, radius + 1, dtype=torch.int32)
+
+
+def relpos_log_borders(num_buckets: int, max_distance: int) -> torch.Tensor:
+    """Borders of log-spaced buckets, symmetric in the sign: half of the buckets
+    for each sign, half of those for single distances and the others for
+    distances that grow by equal factors up to ``max_distance`` (the last one
+    takes all beyond).  Ascending int32 on the CPU, at most num_buckets - 2 of
+    them: equal borders, which small buckets can give, are merged."""
+    half = num_buckets // 2
+    single = half // 2
+    if num_buckets % 2 or single < 1:
+        raise ValueError("num_buckets must be even and at least 4")
+    if not single < max_distance < 2 ** 31:
+        raise ValueError(f"max_distance must be above num_buckets // 4 = {single} and below 2^31")
+    steps, up, t = half - single, list(range(1, single + 1)), single
+    for k in range(1, steps):
+        # the smallest t with (t / single)^steps >= (max_distance / single)^k, decided in whole numbers
+        t = max(t, int(single * (max_distance / single) ** (k / steps)) - 2)
+        while t ** steps * single ** k < max_distance ** k * single ** steps:
+            t += 1
+        up.append(t)
+    up = sorted(set(up))
+    return torch.tensor([1 - t for t in reversed(up)] + up, dtype=torch.int32)
+
+
+def _relpos_args(borders, pos, pos_k, chain, chain_k, device):
+    if pos.dim() != 2:
+        raise ValueError("pos must be [B, Sq]")
+    if pos_k is None:
+        if chain_k is not None and chain_k is not chain:
+            raise ValueError("chain_k given without pos_k")
+        pos_k, chain_k = pos, chain
+    if (chain is None) != (chain_k is None):
+        raise ValueError("chain and chain_k must be given together")
+    if borders.dim() != 1 or pos_k.dim() != 2:
+        raise ValueError("borders must be [num_borders] and pos_k [B, Sk]")
+    B, Sq, Sk = pos.shape[0], pos.shape[1], pos_k.shape[1]
+    for name, t, shape in (("borders", borders, borders.shape), ("pos", pos, (B, Sq)), ("pos_k", pos_k, (B, Sk)),
+                           ("chain", chain, (B, Sq)), ("chain_k", chain_k, (B, Sk))):
+        if t is not None:
+            _same(name, t, shape, torch.int32, device)
+    return pos_k, chain_k, B, Sq, Sk, borders.shape[0]
+
+
+def relpos_bias(table: torch.Tensor, borders: torch.Tensor, pos: torch.Tensor, pos_k: Optional[torch.Tensor] = None,
+                chain: Optional[torch.Tensor] = None, chain_k: Optional[torch.Tensor] = None,
+                base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The learned relative-position bias as a pair bias [B, 1, H, Sq, Sk]:
+    table[r, h] (+ base), r the number of borders <= pos[b, i] - pos_k[b, j], or
+    the table's last row where the chains of i and j differ.
+
+    table: [R, H] bf16, fp16 or fp32, R = len(borders) + 1, one more with
+    chains.  borders: ascending int32 [num_borders] (``relpos_clip_borders``,
+    ``relpos_log_borders`` or any others).  pos: int32 [B, Sq]; pos_k: int32
+    [B, Sk], default pos.  chain, chain_k: int32 like pos and pos_k, or None.
+    base: optional bias [B, 1, H, Sq, Sk] added to it.  All contiguous on one
+    CUDA device.  Runs on ``stream`` (default: the current stream) without
+    synchronising.
+    """
+    if table.dim() != 2:
+        raise ValueError("table must be [R, H]")
+    if table.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {table.dtype}")
+    pos_k, chain_k, B, Sq, Sk, nb = _relpos_args(borders, pos, pos_k, chain, chain_k, table.device)
+    H = table.shape[1]
+    _same("table", table, (nb + 1 + (chain is not None), H), table.dtype, table.device)
+    shape = (B, 1, H, Sq, Sk)
+    if base is not None:
+        _same("base", base, shape, table.dtype, table.device)
+    stream, scope = _call_stream(stream, table.device)
+    if out is None:
+        with scope:
+            out = torch.empty(shape, dtype=table.dtype, device=table.device)
+    else:
+        _same("out", out, shape, table.dtype, table.device)
+    status = evo_relpos_fwd(table.data_ptr(), borders.data_ptr(), pos.data_ptr(), pos_k.data_ptr(), _ptr(chain),
+                            _ptr(chain_k), _ptr(base), out.data_ptr(), B, Sq, Sk, H, nb, _DTYPES[table.dtype],
+                            stream.cuda_stream)
+    if status != EVO_OK:
+        raise EvoAttnError(status, "evo_relpos_fwd")
+    return out
+
+
+def relpos_bias_backward(dpair: torch.Tensor, borders: torch.Tensor, pos: torch.Tensor,
+                         pos_k: Optional[torch.Tensor] = None, chain: Optional[torch.Tensor] = None,
+                         chain_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gradient [R, H] of ``relpos_bias``'s table for the gradient dpair
+    ([B, 1, H, Sq, Sk], as ``evo_attn_backward`` returns it) of its result; the
+    gradient of ``base`` is dpair itself.  ``workspace``: optional uint8 CUDA tensor of
+    ``evo_relpos_bwd_workspace_size`` bytes.  Runs on ``stream`` (default: the
+    current stream) without synchronising."""
+    if dpair.dim() != 5:
+        raise ValueError("dpair must be [B, 1, H, Sq, Sk]")
+    if dpair.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dpair.dtype}")
+    pos_k, chain_k, B, Sq, Sk, nb = _relpos_args(borders, pos, pos_k, chain, chain_k, dpair.device)
+    H = dpair.shape[2]
+    _same("dpair", dpair, (B, 1, H, Sq, Sk), dpair.dtype, dpair.device)
+    stream, scope = _call_stream(stream, dpair.device)
+    has_chain = chain is not None
+    with scope:
+        dtable = torch.empty((nb + 1 + has_chain, H), dtype=dpair.dtype, device=dpair.device)
+        workspace = _workspace(workspace, evo_relpos_bwd_workspace_size(B, Sq, Sk, H, nb, int(has_chain)), dpair.device,
+                               "evo_relpos_bwd_workspace_size")
+    status = evo_relpos_bwd(dpair.data_ptr(), borders.data_ptr(), pos.data_ptr(), pos_k.data_ptr(), _ptr(chain),
+                            _ptr(chain_k), dtable.data_ptr(), workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), B, Sq, Sk, H, nb, _DTYPES[dpair.dtype],
+                            stream.cuda_stream)
+    if status != EVO_OK:
+        raise EvoAttnError(status, "evo_relpos_bwd")
+    return dtable

@@ -13,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,8 +25,11 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
-    "-shared",
 ]
+
+# translation units: attention and triangle multiplication; the transition and
+# the relative-position bias
+UNITS = ["evo_attn.cu", "evo_blocks.cu"]
 
 
 def _nvcc() -> str:
@@ -51,12 +55,23 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and not is_stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC,
-           os.path.join(CSRC, "evo_attn.cu"), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    objs = [f"{tmp}.{os.path.splitext(u)[0]}.o" for u in UNITS]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+
+    try:
+        with ThreadPoolExecutor(len(UNITS)) as pool:
+            list(pool.map(lambda uo: run([_nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-c",
+                                          os.path.join(CSRC, uo[0]), "-o", uo[1]]), zip(UNITS, objs)))
+        run([_nvcc(), *NVCC_FLAGS, "-shared", *objs, "-o", tmp])
+        os.replace(tmp, LIB)
+    finally:
+        for path in (*objs, tmp):
+            if os.path.exists(path):
+                os.remove(path)
     return LIB
 
 

@@ -8,10 +8,10 @@
 
 namespace evo {
 
-// Device status word of this library (one per device that loads it).  A
-// kernel that gives up waiting records EVO_ERR_TIMEOUT here; the host reads
-// and clears it in evo_attn_sync_status().
-__device__ int g_status;
+// Device status word of this library (per device, one for each translation
+// unit's kernels).  A kernel that gives up waiting records EVO_ERR_TIMEOUT here;
+// the host reads and clears the words in evo_attn_sync_status().
+static __device__ int g_status;
 
 // A wait on an internal barrier longer than this is treated as a hang.
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
@@ -20,7 +20,7 @@ constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 __device__ __forceinline__ void record_status(int code) { atomicCAS(&g_status, 0, code); }
 
 // Bounded wait with an explicit limit (the self-test uses a short one).
-__device__ __noinline__ bool wait_bounded_for(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+static __device__ __noinline__ bool wait_bounded_for(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (true) {
         if (ptx::mbar_try_wait(bar, parity)) return true;

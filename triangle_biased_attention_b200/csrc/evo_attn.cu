@@ -21,6 +21,7 @@
 
 #include "evo_attn.h"
 #include "common.cuh"
+#include "host_util.cuh"
 #include "fwd_tri_sm100.cuh"
 #include "fwd_f32.cuh"
 #include "bwd_simt.cuh"
@@ -28,93 +29,6 @@
 #include "trimul_sm100.cuh"
 
 namespace {
-
-
-constexpr int kMaxDevices = 64;
-
-// Sets a kernel's dynamic shared-memory limit once per device.  Calls from
-// several host threads may race on the first use; a mutex orders them and
-// the flag is only set once the attribute call has succeeded.
-struct AttrOnce {
-    std::mutex mu;
-    bool done[kMaxDevices] = {};
-    template <typename K>
-    bool ensure(int dev, K kernel, int smem_bytes) {
-        std::lock_guard<std::mutex> lock(mu);
-        if (done[dev]) return true;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
-            return false;
-        done[dev] = true;
-        return true;
-    }
-};
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
-
-bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-    if (a == nullptr || b == nullptr || abytes <= 0 || bbytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + uint64_t(bbytes) && b0 < a0 + uint64_t(abytes);
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// The device that owns `ptr`, or a negative status if it is not device memory.
-int device_of(const void* ptr) {
-    cudaPointerAttributes attr;
-    if (cudaPointerGetAttributes(&attr, ptr) != cudaSuccess) {
-        cudaGetLastError();
-        return EVO_ERR_INVALID_ARG;
-    }
-    if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) return EVO_ERR_INVALID_ARG;
-    return attr.device;
-}
-
-// Makes the device that owns the buffers current for the duration of one
-// call and restores the caller's current device afterwards.
-struct DeviceScope {
-    int prev = -1;
-    bool changed = false;
-    ~DeviceScope() {
-        if (changed) cudaSetDevice(prev);
-    }
-};
-
-// Relaxed stream-capture mode for this thread during one call, so that the
-// call's host-side queries (pointer attributes, function attributes, the
-// driver entry point) are allowed while the caller captures a CUDA graph;
-// the launches and copies themselves are captured as usual.
-struct RelaxedCapture {
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
-    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
-};
-
-int select_device_of(const void* ptr, DeviceScope& scope) {
-    const int dev = device_of(ptr);
-    if (dev < 0) return dev;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess) return EVO_ERR_CUDA;
-    if (cur != dev) {
-        if (cudaSetDevice(dev) != cudaSuccess) return EVO_ERR_CUDA;
-        scope.prev = cur;
-        scope.changed = true;
-    }
-    return dev;
-}
 
 // Q/K/V/O as a 4-D tensor {D, H, S, B*N}; a box is one (b, n, h) slice's
 // 128 rows of `box_w` elements (D, or 64 for D = 128, whose rows are loaded as
@@ -437,17 +351,11 @@ extern "C" EVO_API int evo_attn_sync_status(evo_stream_t stream) {
         scope.changed = true;
     }
     if (cudaStreamSynchronize(st) != cudaSuccess) return EVO_ERR_CUDA;
-    int v = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, evo::g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess)
-        return EVO_ERR_CUDA;
-    if (cudaStreamSynchronize(st) != cudaSuccess) return EVO_ERR_CUDA;
-    if (v != 0) {
-        const int zero = 0;
-        if (cudaMemcpyToSymbolAsync(evo::g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st) !=
-                cudaSuccess ||
-            cudaStreamSynchronize(st) != cudaSuccess)
-            return EVO_ERR_CUDA;
-    }
+    int v = EVO_OK;
+    if (!take_status_word(evo::g_status, st, &v)) return EVO_ERR_CUDA;
+    int w = EVO_OK;  // the transition and relative-position kernels' word
+    if (evo::take_blocks_status(st, &w) != EVO_OK) return EVO_ERR_CUDA;
+    if (v == EVO_OK) v = w;
     return v;
 }
 

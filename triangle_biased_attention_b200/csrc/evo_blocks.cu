@@ -1,0 +1,513 @@
+// Host side of the operators around the attention: the gated transition and the
+// learned relative-position bias (argument checks, workspace layouts and
+// launches of the C entry points declared in include/evo_attn.h).
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+#include <initializer_list>
+#include <type_traits>
+
+#include "evo_attn.h"
+#include "common.cuh"
+#include "host_util.cuh"
+#include "relpos.cuh"
+#include "transition_simt.cuh"
+
+namespace evo {
+
+int take_blocks_status(cudaStream_t stream, int* status) {
+    return take_status_word(g_status, stream, status) ? EVO_OK : EVO_ERR_CUDA;
+}
+
+}  // namespace evo
+
+namespace {
+
+constexpr int64_t kIntMax = 2147483647;
+
+int64_t elem_bytes(int dtype) { return dtype == EVO_DTYPE_FP32 ? 4 : 2; }
+
+bool dtype_ok(int dtype) { return dtype == EVO_DTYPE_BF16 || dtype == EVO_DTYPE_FP32 || dtype == EVO_DTYPE_FP16; }
+
+int sm_count(int dev) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+struct Buf {
+    const void* p;
+    int64_t bytes;
+    bool written;
+};
+
+// Written buffers must not overlap any other buffer of the call.
+bool any_overlap(std::initializer_list<Buf> bufs) {
+    for (const Buf* a = bufs.begin(); a != bufs.end(); ++a)
+        for (const Buf* b = a + 1; b != bufs.end(); ++b)
+            if ((a->written || b->written) && overlap(a->p, a->bytes, b->p, b->bytes)) return true;
+    return false;
+}
+
+// Every buffer must live on the first one's device; makes it current.
+int select_device(std::initializer_list<const void*> ptrs, DeviceScope& scope) {
+    int dev = -1;
+    for (const void* p : ptrs) {
+        if (p == nullptr) continue;
+        if (dev < 0) {
+            dev = select_device_of(p, scope);
+            if (dev < 0) return dev;
+            if (dev >= kMaxDevices) return EVO_ERR_UNSUPPORTED_SHAPE;
+        } else if (device_of(p) != dev) {
+            return EVO_ERR_INVALID_ARG;
+        }
+    }
+    return dev;
+}
+
+// ------------------------------------------------------------------ transition
+
+// Rows are taken in chunks whose [rows, F] intermediates stay in the 126 MB L2
+// between the kernel that writes them and the ones that read them, and bound
+// the workspace.  A chunk is a whole number of 128-row tiles for each of 148 SMs.
+constexpr int64_t kTrWave = 148 * 128;
+
+int64_t tr_chunk_rows(int64_t M, int64_t row_bytes) {
+    const int64_t target = int64_t(64) << 20;
+    const int64_t waves = std::max<int64_t>(1, target / (kTrWave * std::max<int64_t>(row_bytes, 1)));
+    return std::min(M, waves * kTrWave);
+}
+
+struct TrLayout {
+    int64_t chunk = 0;           // rows of a chunk
+    int64_t h = 0, dg = 0, du = 0;  // [chunk, F]
+    int64_t part = 0;            // [splits][3][F * C] fp32
+    int64_t splits = 0;
+    int64_t total = 0;
+};
+
+// Sections on 256-byte boundaries.  False when a byte count passes int64.
+bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayout* L) {
+    const int64_t es = elem_bytes(dtype);
+    int64_t mc, mf, fc, row_bytes;
+    if (!mul_ok(M, C, &mc) || !mul_ok(M, F, &mf) || !mul_ok(F, C, &fc) || mc > INT64_MAX / 64 || mf > INT64_MAX / 64 ||
+        fc > INT64_MAX / 4096 || !mul_ok(F, es * (backward ? 3 : 1), &row_bytes))
+        return false;
+    L->chunk = tr_chunk_rows(M, row_bytes);
+    int64_t off = 0;
+    auto take = [&off](int64_t bytes) {
+        const int64_t at = off;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    L->h = take(L->chunk * F * es);
+    if (backward) {
+        L->dg = take(L->chunk * F * es);
+        L->du = take(L->chunk * F * es);
+        // enough ranges of rows for two blocks a SM, none under 512 rows
+        const int64_t tiles = 3 * ((F + 127) / 128) * ((C + 127) / 128);
+        L->splits = std::max<int64_t>(1, std::min((296 + tiles - 1) / tiles, (L->chunk + 511) / 512));
+        L->part = take(L->splits * 3 * fc * 4);
+    }
+    L->total = off;
+    return true;
+}
+
+int check_transition(int64_t M, int64_t C, int64_t F, int act, int dtype) {
+    if (M < 0 || C < 0 || F < 0 || (act != EVO_ACT_SILU && act != EVO_ACT_GELU)) return EVO_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return EVO_ERR_UNSUPPORTED_DTYPE;
+    // tile counts and row offsets inside a chunk are 32-bit
+    if (M > kIntMax || C > (1 << 20) || F > (1 << 20)) return EVO_ERR_UNSUPPORTED_SHAPE;
+    return EVO_OK;
+}
+
+constexpr int kTrSmem = 4 * evo::kTrK * evo::kTrLd * int(sizeof(float));
+
+template <typename K, typename P>
+bool launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const P& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
+}
+
+unsigned blocks_of(int64_t n, int64_t tile) { return unsigned((n + tile - 1) / tile); }
+
+template <typename T, int ACT>
+int run_fwd_simt(const T* X, const T* Wg, const T* Wu, const T* Wd, T* Y, char* ws, int64_t M, int64_t C, int64_t F,
+                 int dtype, cudaStream_t st) {
+    TrLayout L;
+    tr_layout(M, C, F, dtype, false, &L);  // checked by the caller
+    evo::TrSimtParams<T> p = {};
+    p.wg = Wg;
+    p.wu = Wu;
+    p.wd = Wd;
+    p.h = reinterpret_cast<T*>(ws + L.h);
+    p.C = int(C);
+    p.F = int(F);
+    p.vec = sizeof(T) == 4 && C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
+            aligned(Wd, 16) && aligned(Y, 16);
+    for (int64_t m = 0; m < M; m += L.chunk) {
+        p.rows = int(std::min(L.chunk, M - m));
+        p.x = X + m * C;
+        p.out = Y + m * C;
+        const unsigned mt = blocks_of(p.rows, 128);
+        if (!launch(evo::evo_tr_simt_gate_kernel<T, ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
+            !launch(evo::evo_tr_simt_out_kernel<T, false>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem, st, p))
+            return EVO_ERR_CUDA;
+    }
+    return EVO_OK;
+}
+
+template <typename T, int ACT>
+int run_bwd_simt(const T* X, const T* Wg, const T* Wu, const T* Wd, const T* dY, T* dX, T* dWg, T* dWu, T* dWd,
+                 char* ws, int64_t M, int64_t C, int64_t F, int dtype, cudaStream_t st) {
+    TrLayout L;
+    tr_layout(M, C, F, dtype, true, &L);
+    evo::TrSimtParams<T> p = {};
+    p.wg = Wg;
+    p.wu = Wu;
+    p.wd = Wd;
+    p.h = reinterpret_cast<T*>(ws + L.h);
+    p.dg = reinterpret_cast<T*>(ws + L.dg);
+    p.du = reinterpret_cast<T*>(ws + L.du);
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.C = int(C);
+    p.F = int(F);
+    p.splits = int(L.splits);
+    p.split_rows = int((L.chunk + L.splits - 1) / L.splits);
+    p.dw_mask = (dWg ? 1 : 0) | (dWu ? 2 : 0) | (dWd ? 4 : 0);
+    p.vec = sizeof(T) == 4 && C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
+            aligned(Wd, 16) && aligned(dY, 16) && (!dX || aligned(dX, 16));
+    for (int64_t m = 0; m < M; m += L.chunk) {
+        p.rows = int(std::min(L.chunk, M - m));
+        p.x = X + m * C;
+        p.dy = dY + m * C;
+        p.out = dX ? dX + m * C : nullptr;
+        p.first = m == 0;
+        const unsigned mt = blocks_of(p.rows, 128), big = blocks_of(std::max(C, F), 128);
+        if (!launch(evo::evo_tr_simt_grad_kernel<T, ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
+            (dX && !launch(evo::evo_tr_simt_out_kernel<T, true>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem,
+                           st, p)) ||
+            (p.dw_mask && !launch(evo::evo_tr_simt_dw_kernel<T>, dim3(big, big, unsigned(3 * L.splits)),
+                                  evo::kTrThreads, kTrSmem, st, p)))
+            return EVO_ERR_CUDA;
+    }
+    if (p.dw_mask) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(blocks_of(F * C, 256), 1, 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        cfg.stream = st;
+        if (cudaLaunchKernelEx(&cfg, evo::evo_tr_dw_reduce_kernel<T>, (const float*)p.part, p.splits, (long long)(F * C),
+                               dWg, dWu, dWd) != cudaSuccess)
+            return EVO_ERR_CUDA;
+    }
+    return EVO_OK;
+}
+
+#define EVO_TR_DISPATCH(RUN, ...)                                                          \
+    if (dtype == EVO_DTYPE_FP32) {                                                         \
+        using T = float;                                                                   \
+        return act == EVO_ACT_SILU ? RUN<T, EVO_ACT_SILU> __VA_ARGS__ : RUN<T, EVO_ACT_GELU> __VA_ARGS__; \
+    }                                                                                      \
+    if (dtype == EVO_DTYPE_FP16) {                                                         \
+        using T = __half;                                                                  \
+        return act == EVO_ACT_SILU ? RUN<T, EVO_ACT_SILU> __VA_ARGS__ : RUN<T, EVO_ACT_GELU> __VA_ARGS__; \
+    }                                                                                      \
+    using T = __nv_bfloat16;                                                               \
+    return act == EVO_ACT_SILU ? RUN<T, EVO_ACT_SILU> __VA_ARGS__ : RUN<T, EVO_ACT_GELU> __VA_ARGS__
+
+int64_t tr_workspace(int64_t M, int64_t C, int64_t F, int dtype, bool backward) {
+    const int st = check_transition(M, C, F, EVO_ACT_SILU, dtype);
+    if (st != EVO_OK) return st;
+    if (M == 0 || C == 0 || F == 0) return 0;
+    TrLayout L;
+    if (!tr_layout(M, C, F, dtype, backward, &L)) return EVO_ERR_UNSUPPORTED_SHAPE;
+    return L.total;
+}
+
+// the alignment every tensor of a transition call needs
+uintptr_t tr_alignment(int64_t C, int64_t F, int dtype) {
+    if (dtype == EVO_DTYPE_FP32) return 4;
+    return C % 8 == 0 && F % 8 == 0 ? 16 : 2;
+}
+
+bool zero(void* p, int64_t bytes, cudaStream_t st) {
+    return p == nullptr || bytes == 0 || cudaMemsetAsync(p, 0, size_t(bytes), st) == cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" EVO_API int64_t evo_transition_fwd_workspace_size(int64_t M, int64_t C, int64_t F, int dtype) {
+    return tr_workspace(M, C, F, dtype, false);
+}
+
+extern "C" EVO_API int64_t evo_transition_bwd_workspace_size(int64_t M, int64_t C, int64_t F, int dtype) {
+    return tr_workspace(M, C, F, dtype, true);
+}
+
+extern "C" EVO_API int evo_transition_fwd(const void* X, const void* Wg, const void* Wu, const void* Wd, void* Y,
+                                          void* workspace, int64_t workspace_bytes, int64_t M, int64_t C, int64_t F,
+                                          int act, int dtype, evo_stream_t stream) {
+    const int chk = check_transition(M, C, F, act, dtype);
+    if (chk != EVO_OK) return chk;
+    if (workspace_bytes < 0) return EVO_ERR_INVALID_ARG;
+    if (M == 0 || C == 0) return EVO_OK;  // Y is empty
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t es = elem_bytes(dtype);
+    if (!Y || (F > 0 && (!X || !Wg || !Wu || !Wd || !workspace))) return EVO_ERR_INVALID_ARG;
+    TrLayout L;
+    if (F > 0 && !tr_layout(M, C, F, dtype, false, &L)) return EVO_ERR_UNSUPPORTED_SHAPE;
+    const int64_t xb = M * C * es, wb = F * C * es;
+    if (F > 0) {
+        if (workspace_bytes < L.total) return EVO_ERR_INVALID_ARG;
+        for (const void* p : {X, Wg, Wu, Wd, static_cast<const void*>(Y)})
+            if (!aligned(p, tr_alignment(C, F, dtype))) return EVO_ERR_MISALIGNED;
+        if (!aligned(workspace, 256)) return EVO_ERR_MISALIGNED;
+        if (any_overlap({{Y, xb, true}, {workspace, L.total, true}, {X, xb, false}, {Wg, wb, false}, {Wu, wb, false},
+                         {Wd, wb, false}}))
+            return EVO_ERR_INVALID_ARG;
+    }
+    RelaxedCapture relaxed;
+    DeviceScope scope;
+    if (F == 0) {  // an empty sum
+        const int dev = select_device({Y}, scope);
+        return dev < 0 ? dev : zero(Y, xb, st) ? EVO_OK : EVO_ERR_CUDA;
+    }
+    const int dev = select_device({X, Wg, Wu, Wd, Y, workspace}, scope);
+    if (dev < 0) return dev;
+    char* ws = static_cast<char*>(workspace);
+    EVO_TR_DISPATCH(run_fwd_simt, (static_cast<const T*>(X), static_cast<const T*>(Wg), static_cast<const T*>(Wu),
+                                   static_cast<const T*>(Wd), static_cast<T*>(Y), ws, M, C, F, dtype, st));
+}
+
+extern "C" EVO_API int evo_transition_bwd(const void* X, const void* Wg, const void* Wu, const void* Wd,
+                                          const void* dY, void* dX, void* dWg, void* dWu, void* dWd, void* workspace,
+                                          int64_t workspace_bytes, int64_t M, int64_t C, int64_t F, int act, int dtype,
+                                          evo_stream_t stream) {
+    const int chk = check_transition(M, C, F, act, dtype);
+    if (chk != EVO_OK) return chk;
+    if (workspace_bytes < 0) return EVO_ERR_INVALID_ARG;
+    if (C == 0 || (!dX && !dWg && !dWu && !dWd)) return EVO_OK;  // nothing to write
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t es = elem_bytes(dtype);
+    const bool empty = M == 0 || F == 0;
+    if (!empty && (!X || !Wg || !Wu || !Wd || !dY || !workspace)) return EVO_ERR_INVALID_ARG;
+    TrLayout L;
+    if (!empty && !tr_layout(M, C, F, dtype, true, &L)) return EVO_ERR_UNSUPPORTED_SHAPE;
+    const int64_t xb = M * C * es, wb = F * C * es;
+    for (const void* p : {X, Wg, Wu, Wd, dY, static_cast<const void*>(dX), static_cast<const void*>(dWg),
+                          static_cast<const void*>(dWu), static_cast<const void*>(dWd)})
+        if (p && !aligned(p, tr_alignment(C, F, dtype))) return EVO_ERR_MISALIGNED;
+    if (!empty) {
+        if (workspace_bytes < L.total) return EVO_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return EVO_ERR_MISALIGNED;
+    }
+    if (any_overlap({{dX, xb, true}, {dWg, wb, true}, {dWu, wb, true}, {dWd, wb, true},
+                     {workspace, empty ? 0 : L.total, true}, {X, xb, false}, {dY, xb, false}, {Wg, wb, false},
+                     {Wu, wb, false}, {Wd, wb, false}}))
+        return EVO_ERR_INVALID_ARG;
+    RelaxedCapture relaxed;
+    DeviceScope scope;
+    if (empty) {  // empty sums
+        if (xb == 0) dX = nullptr;
+        if (wb == 0) dWg = dWu = dWd = nullptr;
+        if (!dX && !dWg && !dWu && !dWd) return EVO_OK;
+        const int dev = select_device({dX, dWg, dWu, dWd}, scope);
+        if (dev < 0) return dev;
+        return zero(dX, xb, st) && zero(dWg, wb, st) && zero(dWu, wb, st) && zero(dWd, wb, st) ? EVO_OK : EVO_ERR_CUDA;
+    }
+    const int dev = select_device({X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, workspace}, scope);
+    if (dev < 0) return dev;
+    char* ws = static_cast<char*>(workspace);
+    EVO_TR_DISPATCH(run_bwd_simt, (static_cast<const T*>(X), static_cast<const T*>(Wg), static_cast<const T*>(Wu),
+                                   static_cast<const T*>(Wd), static_cast<const T*>(dY), static_cast<T*>(dX),
+                                   static_cast<T*>(dWg), static_cast<T*>(dWu), static_cast<T*>(dWd), ws, M, C, F, dtype,
+                                   st));
+}
+
+// ------------------------------------------------- relative-position bias
+
+namespace {
+
+int check_relpos(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t nb, int dtype) {
+    if (B < 0 || Sq < 0 || Sk < 0 || H < 0 || nb < 0) return EVO_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return EVO_ERR_UNSUPPORTED_DTYPE;
+    if (nb > evo::kRelMaxBorders || B > 65535 || Sq > kIntMax / 4 || Sk > kIntMax / 4 || H > 65535)
+        return EVO_ERR_UNSUPPORTED_SHAPE;
+    int64_t n;
+    if (!mul_ok(B * H, Sq, &n) || !mul_ok(n, Sk, &n) || n > INT64_MAX / 16) return EVO_ERR_UNSUPPORTED_SHAPE;
+    return EVO_OK;
+}
+
+// Threads of a block along j, as a power of two: no more than the key columns need.
+int rel_lane_cols(int64_t Sk, int most) {
+    int l = 0;
+    while (l < most && (int64_t(evo::kRelCols) << l) < Sk) ++l;
+    return l;
+}
+
+struct RelTiles {
+    int lane_cols, ti;
+    int64_t jt, it, chunks;
+    int64_t part_bytes;
+};
+
+// Backward blocks: a tile of query rows high enough that its rows outweigh
+// clearing and adding up the block's bins, low enough that the blocks fill the SMs.
+RelTiles rel_bwd_tiles(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t rows) {
+    RelTiles t;
+    t.lane_cols = rel_lane_cols(Sk, 7);
+    t.jt = (Sk + (int64_t(evo::kRelCols) << t.lane_cols) - 1) / (int64_t(evo::kRelCols) << t.lane_cols);
+    t.chunks = (rows + evo::kRelBins - 1) / evo::kRelBins;
+    const int64_t per = evo::kRelBwdThreads >> t.lane_cols;  // query rows at once
+    const int64_t others = std::max<int64_t>(1, B * H * t.jt);
+    const int64_t want = std::max<int64_t>(1, 148 * 6 / others);
+    int64_t ti = std::max<int64_t>((Sq + want - 1) / want, 16 * per);
+    ti = std::max<int64_t>(ti, (Sq + 65534) / 65535);
+    t.ti = int(std::min<int64_t>((ti + per - 1) / per * per, kIntMax / 4));
+    t.it = (Sq + t.ti - 1) / t.ti;
+    t.part_bytes = B * t.it * t.jt * H * rows * 4;
+    return t;
+}
+
+template <typename T>
+int run_relpos_fwd(evo::RelParams<T> p, const void* table, const void* base, void* pair, cudaStream_t st) {
+    p.table = static_cast<const T*>(table);
+    p.base = static_cast<const T*>(base);
+    p.pair = static_cast<T*>(pair);
+    p.lane_cols = rel_lane_cols(p.Sk, 8);
+    const int64_t cols = int64_t(evo::kRelCols) << p.lane_cols;
+    const int64_t jt = (p.Sk + cols - 1) / cols;
+    const int per = evo::kRelThreads >> p.lane_cols;
+    int64_t ti = std::max<int64_t>(4 * per, (int64_t(p.Sq) + 65534) / 65535);
+    p.ti = int((ti + per - 1) / per * per);
+    const dim3 grid{unsigned(jt), blocks_of(p.Sq, p.ti), unsigned(p.B)};
+    return launch(evo::evo_relpos_fwd_kernel<T>, grid, evo::kRelThreads, 0, st, p) ? EVO_OK : EVO_ERR_CUDA;
+}
+
+template <typename T>
+int run_relpos_bwd(int dev, evo::RelParams<T> p, const void* dpair, void* dtable, void* ws, cudaStream_t st) {
+    const RelTiles t = rel_bwd_tiles(p.B, p.Sq, p.Sk, p.H, p.rows);
+    p.dpair = static_cast<const T*>(dpair);
+    p.part = static_cast<float*>(ws);
+    p.lane_cols = t.lane_cols;
+    p.ti = t.ti;
+    auto kernel = evo::evo_relpos_bwd_kernel<T>;
+    static AttrOnce attr;
+    if (!attr.ensure(dev, kernel, evo::kRelBins * evo::kRelBwdThreads * 4)) return EVO_ERR_CUDA;
+    const int smem = std::min(p.rows, evo::kRelBins) * evo::kRelBwdThreads * 4;
+    const dim3 grid{unsigned(t.jt), unsigned(t.it), unsigned(p.B * p.H * t.chunks)};
+    if (!launch(kernel, grid, evo::kRelBwdThreads, smem, st, p)) return EVO_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks_of(int64_t(p.H) * p.rows, 8), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, evo::evo_relpos_bwd_sum_kernel<T>, (const float*)p.part,
+                              (long long)(p.B * t.it * t.jt), p.H, p.rows, static_cast<T*>(dtable)) == cudaSuccess
+               ? EVO_OK
+               : EVO_ERR_CUDA;
+}
+
+template <typename T>
+evo::RelParams<T> rel_params(const int32_t* borders, const int32_t* pos_q, const int32_t* pos_k, const int32_t* chain_q,
+                             const int32_t* chain_k, int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t nb) {
+    evo::RelParams<T> p = {};
+    p.borders = borders;
+    p.pos_q = pos_q;
+    p.pos_k = pos_k;
+    p.chain_q = chain_q;
+    p.chain_k = chain_k;
+    p.B = int(B);
+    p.Sq = int(Sq);
+    p.Sk = int(Sk);
+    p.H = int(H);
+    p.nb = int(nb);
+    p.rows = int(nb) + 1 + (chain_q != nullptr);
+    return p;
+}
+
+}  // namespace
+
+extern "C" EVO_API int evo_relpos_fwd(const void* table, const int32_t* borders, const int32_t* pos_q,
+                                      const int32_t* pos_k, const int32_t* chain_q, const int32_t* chain_k,
+                                      const void* base, void* pair, int64_t B, int64_t Sq, int64_t Sk, int64_t H,
+                                      int64_t num_borders, int dtype, evo_stream_t stream) {
+    const int chk = check_relpos(B, Sq, Sk, H, num_borders, dtype);
+    if (chk != EVO_OK) return chk;
+    if ((chain_q == nullptr) != (chain_k == nullptr)) return EVO_ERR_INVALID_ARG;
+    if (B == 0 || Sq == 0 || Sk == 0 || H == 0) return EVO_OK;
+    if (!table || (!borders && num_borders > 0) || !pos_q || !pos_k || !pair) return EVO_ERR_INVALID_ARG;
+    const int64_t es = elem_bytes(dtype), pb = B * H * Sq * Sk * es;
+    for (const void* p : {table, base, static_cast<const void*>(pair)})
+        if (p && !aligned(p, uintptr_t(es))) return EVO_ERR_MISALIGNED;
+    for (const int32_t* p : {borders, pos_q, pos_k, chain_q, chain_k})
+        if (p && !aligned(p, 4)) return EVO_ERR_MISALIGNED;
+    const int64_t rows = num_borders + 1 + (chain_q != nullptr);
+    if (any_overlap({{pair, pb, true}, {table, rows * H * es, false}, {borders, num_borders * 4, false},
+                     {pos_q, B * Sq * 4, false}, {pos_k, B * Sk * 4, false}, {chain_q, B * Sq * 4, false},
+                     {chain_k, B * Sk * 4, false}, {base, pb, false}}))
+        return EVO_ERR_INVALID_ARG;
+    RelaxedCapture relaxed;
+    DeviceScope scope;
+    const int dev = select_device({pair, table, num_borders ? borders : nullptr, pos_q, pos_k, chain_q, chain_k, base}, scope);
+    if (dev < 0) return dev;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+#define EVO_REL_FWD(T) \
+    return run_relpos_fwd<T>(rel_params<T>(borders, pos_q, pos_k, chain_q, chain_k, B, Sq, Sk, H, num_borders), table, base, pair, st)
+    if (dtype == EVO_DTYPE_FP32) EVO_REL_FWD(float);
+    if (dtype == EVO_DTYPE_FP16) EVO_REL_FWD(__half);
+    EVO_REL_FWD(__nv_bfloat16);
+#undef EVO_REL_FWD
+}
+
+extern "C" EVO_API int64_t evo_relpos_bwd_workspace_size(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t num_borders,
+                                                         int has_chain) {
+    const int chk = check_relpos(B, Sq, Sk, H, num_borders, EVO_DTYPE_BF16);
+    if (chk != EVO_OK) return chk;
+    if (B == 0 || Sq == 0 || Sk == 0 || H == 0) return 0;
+    return rel_bwd_tiles(B, Sq, Sk, H, num_borders + 1 + (has_chain != 0)).part_bytes;
+}
+
+extern "C" EVO_API int evo_relpos_bwd(const void* dpair, const int32_t* borders, const int32_t* pos_q,
+                                      const int32_t* pos_k, const int32_t* chain_q, const int32_t* chain_k, void* dtable,
+                                      void* workspace, int64_t workspace_bytes, int64_t B, int64_t Sq, int64_t Sk,
+                                      int64_t H, int64_t num_borders, int dtype, evo_stream_t stream) {
+    const int chk = check_relpos(B, Sq, Sk, H, num_borders, dtype);
+    if (chk != EVO_OK) return chk;
+    if (workspace_bytes < 0 || (chain_q == nullptr) != (chain_k == nullptr)) return EVO_ERR_INVALID_ARG;
+    if (H == 0) return EVO_OK;
+    if (!dtable) return EVO_ERR_INVALID_ARG;
+    const int64_t es = elem_bytes(dtype), pb = B * H * Sq * Sk * es;
+    const int64_t rows = num_borders + 1 + (chain_q != nullptr), tb = rows * H * es;
+    if (!aligned(dtable, uintptr_t(es))) return EVO_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    RelaxedCapture relaxed;
+    DeviceScope scope;
+    if (pb == 0) {  // no pair: an empty sum
+        const int dev = select_device({dtable}, scope);
+        return dev < 0 ? dev : zero(dtable, tb, st) ? EVO_OK : EVO_ERR_CUDA;
+    }
+    if (!dpair || (!borders && num_borders > 0) || !pos_q || !pos_k || !workspace) return EVO_ERR_INVALID_ARG;
+    const RelTiles t = rel_bwd_tiles(B, Sq, Sk, H, rows);
+    if (B * H * t.chunks > 65535) return EVO_ERR_UNSUPPORTED_SHAPE;
+    if (workspace_bytes < t.part_bytes) return EVO_ERR_INVALID_ARG;
+    if (!aligned(dpair, uintptr_t(es)) || !aligned(workspace, 256)) return EVO_ERR_MISALIGNED;
+    for (const int32_t* p : {borders, pos_q, pos_k, chain_q, chain_k})
+        if (p && !aligned(p, 4)) return EVO_ERR_MISALIGNED;
+    if (any_overlap({{dtable, tb, true}, {workspace, t.part_bytes, true}, {borders, num_borders * 4, false},
+                     {pos_q, B * Sq * 4, false}, {pos_k, B * Sk * 4, false}, {chain_q, B * Sq * 4, false},
+                     {chain_k, B * Sk * 4, false}, {dpair, pb, false}}))
+        return EVO_ERR_INVALID_ARG;
+    const int dev = select_device({dpair, dtable, workspace, num_borders ? borders : nullptr, pos_q, pos_k, chain_q, chain_k}, scope);
+    if (dev < 0) return dev;
+#define EVO_REL_BWD(T)                                                                                             \
+    return run_relpos_bwd<T>(dev, rel_params<T>(borders, pos_q, pos_k, chain_q, chain_k, B, Sq, Sk, H, num_borders), \
+                             dpair, dtable, workspace, st)
+    if (dtype == EVO_DTYPE_FP32) EVO_REL_BWD(float);
+    if (dtype == EVO_DTYPE_FP16) EVO_REL_BWD(__half);
+    EVO_REL_BWD(__nv_bfloat16);
+#undef EVO_REL_BWD
+}
