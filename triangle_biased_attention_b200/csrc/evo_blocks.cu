@@ -12,6 +12,7 @@
 #include "host_util.cuh"
 #include "relpos.cuh"
 #include "transition_simt.cuh"
+#include "transition_sm100.cuh"
 
 namespace evo {
 
@@ -78,36 +79,58 @@ int64_t tr_chunk_rows(int64_t M, int64_t row_bytes) {
     return std::min(M, waves * kTrWave);
 }
 
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
 struct TrLayout {
-    int64_t chunk = 0;           // rows of a chunk
-    int64_t h = 0, dg = 0, du = 0;  // [chunk, F]
-    int64_t part = 0;            // [splits][3][F * C] fp32
-    int64_t splits = 0;
+    int64_t chunk = 0;                            // rows of a chunk
+    int64_t h = 0, dg = 0, du = 0;                // [chunk, F] (16-bit: rows up to 128, F up to 128)
+    int64_t part = 0;                             // partial weight gradients, fp32
+    int64_t splits = 0, split_rows = 0;           // ranges of rows with a slot of their own
+    int64_t x = 0, dy = 0, wg = 0, wu = 0, wd = 0;  // 16-bit, odd C or F: copies with rows of whole 16-byte units
+    bool pad = false;
     int64_t total = 0;
 };
 
 // Sections on 256-byte boundaries.  False when a byte count passes int64.
 bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayout* L) {
     const int64_t es = elem_bytes(dtype);
-    int64_t mc, mf, fc, row_bytes;
-    if (!mul_ok(M, C, &mc) || !mul_ok(M, F, &mf) || !mul_ok(F, C, &fc) || mc > INT64_MAX / 64 || mf > INT64_MAX / 64 ||
-        fc > INT64_MAX / 4096 || !mul_ok(F, es * (backward ? 3 : 1), &row_bytes))
-        return false;
-    L->chunk = tr_chunk_rows(M, row_bytes);
+    // C, F <= 2^20 and M < 2^31 (check_transition): the products below fit
+    const int64_t fc = F * C;
+    const int64_t ldf = dtype == EVO_DTYPE_FP32 ? F : round_up(F, 128);
+    L->chunk = tr_chunk_rows(M, ldf * es * (backward ? 3 : 1));
+    const int64_t hbytes = (dtype == EVO_DTYPE_FP32 ? L->chunk : round_up(L->chunk, 128)) * ldf * es;
     int64_t off = 0;
     auto take = [&off](int64_t bytes) {
         const int64_t at = off;
-        off += (bytes + 255) / 256 * 256;
+        off += round_up(bytes, 256);
         return at;
     };
-    L->h = take(L->chunk * F * es);
+    L->h = take(hbytes);
     if (backward) {
-        L->dg = take(L->chunk * F * es);
-        L->du = take(L->chunk * F * es);
-        // enough ranges of rows for two blocks a SM, none under 512 rows
-        const int64_t tiles = 3 * ((F + 127) / 128) * ((C + 127) / 128);
-        L->splits = std::max<int64_t>(1, std::min((296 + tiles - 1) / tiles, (L->chunk + 511) / 512));
-        L->part = take(L->splits * 3 * fc * 4);
+        L->dg = take(hbytes);
+        L->du = take(hbytes);
+        if (dtype == EVO_DTYPE_FP32) {
+            // enough ranges of rows for two blocks a SM, none under 512 rows
+            const int64_t tiles = 3 * ((F + 127) / 128) * ((C + 127) / 128);
+            L->splits = std::max<int64_t>(1, std::min((296 + tiles - 1) / tiles, (L->chunk + 511) / 512));
+            L->split_rows = (L->chunk + L->splits - 1) / L->splits;
+            L->part = take(L->splits * 3 * fc * 4);
+        } else {
+            // as many ranges as keep the tiles within one wave of 148 SMs, none under 512 rows
+            const int64_t tiles = 3 * ((F + 255) / 256) * ((C + 127) / 128);
+            L->splits = std::max<int64_t>(1, std::min(148 / tiles, (L->chunk + 511) / 512));
+            L->split_rows = round_up((L->chunk + L->splits - 1) / L->splits, 64);
+            L->part = take(L->splits * 3 * round_up(C, 128) * round_up(F, 256) * 4);
+        }
+    }
+    L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
+    if (L->pad) {
+        const int64_t cp = round_up(C, 8), fp = round_up(F, 8);
+        L->x = take(L->chunk * cp * 2);
+        if (backward) L->dy = take(L->chunk * cp * 2);
+        L->wg = take(F * cp * 2);
+        L->wu = take(F * cp * 2);
+        L->wd = take(C * fp * 2);
     }
     L->total = off;
     return true;
@@ -135,51 +158,51 @@ bool launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const P
 
 unsigned blocks_of(int64_t n, int64_t tile) { return unsigned((n + tile - 1) / tile); }
 
-template <typename T, int ACT>
-int run_fwd_simt(const T* X, const T* Wg, const T* Wu, const T* Wd, T* Y, char* ws, int64_t M, int64_t C, int64_t F,
+template <int ACT>
+int run_fwd_simt(const float* X, const float* Wg, const float* Wu, const float* Wd, float* Y, char* ws, int64_t M, int64_t C, int64_t F,
                  int dtype, cudaStream_t st) {
     TrLayout L;
     tr_layout(M, C, F, dtype, false, &L);  // checked by the caller
-    evo::TrSimtParams<T> p = {};
+    evo::TrSimtParams p = {};
     p.wg = Wg;
     p.wu = Wu;
     p.wd = Wd;
-    p.h = reinterpret_cast<T*>(ws + L.h);
+    p.h = reinterpret_cast<float*>(ws + L.h);
     p.C = int(C);
     p.F = int(F);
-    p.vec = sizeof(T) == 4 && C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
+    p.vec = C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
             aligned(Wd, 16) && aligned(Y, 16);
     for (int64_t m = 0; m < M; m += L.chunk) {
         p.rows = int(std::min(L.chunk, M - m));
         p.x = X + m * C;
         p.out = Y + m * C;
         const unsigned mt = blocks_of(p.rows, 128);
-        if (!launch(evo::evo_tr_simt_gate_kernel<T, ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
-            !launch(evo::evo_tr_simt_out_kernel<T, false>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem, st, p))
+        if (!launch(evo::evo_tr_simt_gate_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
+            !launch(evo::evo_tr_simt_out_kernel<false>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem, st, p))
             return EVO_ERR_CUDA;
     }
     return EVO_OK;
 }
 
-template <typename T, int ACT>
-int run_bwd_simt(const T* X, const T* Wg, const T* Wu, const T* Wd, const T* dY, T* dX, T* dWg, T* dWu, T* dWd,
+template <int ACT>
+int run_bwd_simt(const float* X, const float* Wg, const float* Wu, const float* Wd, const float* dY, float* dX, float* dWg, float* dWu, float* dWd,
                  char* ws, int64_t M, int64_t C, int64_t F, int dtype, cudaStream_t st) {
     TrLayout L;
     tr_layout(M, C, F, dtype, true, &L);
-    evo::TrSimtParams<T> p = {};
+    evo::TrSimtParams p = {};
     p.wg = Wg;
     p.wu = Wu;
     p.wd = Wd;
-    p.h = reinterpret_cast<T*>(ws + L.h);
-    p.dg = reinterpret_cast<T*>(ws + L.dg);
-    p.du = reinterpret_cast<T*>(ws + L.du);
+    p.h = reinterpret_cast<float*>(ws + L.h);
+    p.dg = reinterpret_cast<float*>(ws + L.dg);
+    p.du = reinterpret_cast<float*>(ws + L.du);
     p.part = reinterpret_cast<float*>(ws + L.part);
     p.C = int(C);
     p.F = int(F);
     p.splits = int(L.splits);
-    p.split_rows = int((L.chunk + L.splits - 1) / L.splits);
+    p.split_rows = int(L.split_rows);
     p.dw_mask = (dWg ? 1 : 0) | (dWu ? 2 : 0) | (dWd ? 4 : 0);
-    p.vec = sizeof(T) == 4 && C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
+    p.vec = C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
             aligned(Wd, 16) && aligned(dY, 16) && (!dX || aligned(dX, 16));
     for (int64_t m = 0; m < M; m += L.chunk) {
         p.rows = int(std::min(L.chunk, M - m));
@@ -188,10 +211,10 @@ int run_bwd_simt(const T* X, const T* Wg, const T* Wu, const T* Wd, const T* dY,
         p.out = dX ? dX + m * C : nullptr;
         p.first = m == 0;
         const unsigned mt = blocks_of(p.rows, 128), big = blocks_of(std::max(C, F), 128);
-        if (!launch(evo::evo_tr_simt_grad_kernel<T, ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
-            (dX && !launch(evo::evo_tr_simt_out_kernel<T, true>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem,
+        if (!launch(evo::evo_tr_simt_grad_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
+            (dX && !launch(evo::evo_tr_simt_out_kernel<true>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem,
                            st, p)) ||
-            (p.dw_mask && !launch(evo::evo_tr_simt_dw_kernel<T>, dim3(big, big, unsigned(3 * L.splits)),
+            (p.dw_mask && !launch(evo::evo_tr_simt_dw_kernel, dim3(big, big, unsigned(3 * L.splits)),
                                   evo::kTrThreads, kTrSmem, st, p)))
             return EVO_ERR_CUDA;
     }
@@ -200,24 +223,201 @@ int run_bwd_simt(const T* X, const T* Wg, const T* Wu, const T* Wd, const T* dY,
         cfg.gridDim = dim3(blocks_of(F * C, 256), 1, 1);
         cfg.blockDim = dim3(256, 1, 1);
         cfg.stream = st;
-        if (cudaLaunchKernelEx(&cfg, evo::evo_tr_dw_reduce_kernel<T>, (const float*)p.part, p.splits, (long long)(F * C),
+        if (cudaLaunchKernelEx(&cfg, evo::evo_tr_dw_reduce_kernel, (const float*)p.part, p.splits, (long long)(F * C),
                                dWg, dWu, dWd) != cudaSuccess)
             return EVO_ERR_CUDA;
     }
     return EVO_OK;
 }
 
-#define EVO_TR_DISPATCH(RUN, ...)                                                          \
-    if (dtype == EVO_DTYPE_FP32) {                                                         \
-        using T = float;                                                                   \
-        return act == EVO_ACT_SILU ? RUN<T, EVO_ACT_SILU> __VA_ARGS__ : RUN<T, EVO_ACT_GELU> __VA_ARGS__; \
-    }                                                                                      \
-    if (dtype == EVO_DTYPE_FP16) {                                                         \
-        using T = __half;                                                                  \
-        return act == EVO_ACT_SILU ? RUN<T, EVO_ACT_SILU> __VA_ARGS__ : RUN<T, EVO_ACT_GELU> __VA_ARGS__; \
-    }                                                                                      \
-    using T = __nv_bfloat16;                                                               \
-    return act == EVO_ACT_SILU ? RUN<T, EVO_ACT_SILU> __VA_ARGS__ : RUN<T, EVO_ACT_GELU> __VA_ARGS__
+// A 16-bit matrix of `rows` rows of `cols` elements, `ld` apart; a box is 64
+// columns (128 B rows, 128 B swizzle) of `box_rows` rows.
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f16) {
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld * 2)};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode_fn()(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                       const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One product over one chunk of rows, a CTA per SM.
+template <int KIND, int ACT, bool F16, int BN>
+int launch_mma(int dev, int sms, const evo::TrMaps& maps, const evo::TrMmaParams& p, cudaStream_t st) {
+    using Cfg = evo::TrCfg<KIND, BN, F16>;
+    auto kernel = evo::evo_tr_mma_kernel<KIND, ACT, F16, BN>;
+    static AttrOnce attr;
+    if (!attr.ensure(dev, kernel, Cfg::SMEM_BYTES)) return EVO_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min(p.num_tiles, sms)), 1, 1);
+    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p) == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+// What a 16-bit call reads through TMA: the tensors themselves, or copies with
+// rows of whole 16-byte units.
+struct TrSource {
+    const void *x, *dy, *wg, *wu, *wd;
+    int64_t ldc, ldf;  // row strides of x, dy, wg, wu and of wd
+};
+
+bool pad_rows(const void* src, void* dst, int64_t rows, int64_t w, int64_t wp, int sms, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>((rows * w + 1023) / 1024, int64_t(sms) * 8)), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, evo::evo_tr_pad_kernel, static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst),
+                              (long long)rows, int(w), int(wp)) == cudaSuccess;
+}
+
+int pad_weights(const TrLayout& L, char* ws, TrSource* s, int64_t C, int64_t F, int sms, cudaStream_t st) {
+    s->ldc = round_up(C, 8);
+    s->ldf = round_up(F, 8);
+    if (!pad_rows(s->wg, ws + L.wg, F, C, s->ldc, sms, st) || !pad_rows(s->wu, ws + L.wu, F, C, s->ldc, sms, st) ||
+        !pad_rows(s->wd, ws + L.wd, C, F, s->ldf, sms, st))
+        return EVO_ERR_CUDA;
+    s->wg = ws + L.wg;
+    s->wu = ws + L.wu;
+    s->wd = ws + L.wd;
+    return EVO_OK;
+}
+
+// Widest stores that rows of C 16-bit elements from `p` allow.
+int wide_store(const void* p, int64_t C) {
+    return C % 16 == 0 && aligned(p, 32) ? 2 : C % 8 == 0 && aligned(p, 16) ? 1 : 0;
+}
+
+int tiles_of(int64_t n, int64_t tile) { return int((n + tile - 1) / tile); }
+
+// Y or dX of one chunk: 256 channels a tile where there are more than 128.
+template <int KIND, bool F16>
+int launch_out(int dev, int sms, const evo::TrMaps& maps, evo::TrMmaParams p, cudaStream_t st) {
+    p.tiles_m = tiles_of(p.rows, 128);
+    p.tiles_n = tiles_of(p.C, p.C > 128 ? 256 : 128);
+    p.num_tiles = p.tiles_m * p.tiles_n;
+    p.kb = tiles_of(p.F, 64);
+    return p.C > 128 ? launch_mma<KIND, 0, F16, 256>(dev, sms, maps, p, st)
+                     : launch_mma<KIND, 0, F16, 128>(dev, sms, maps, p, st);
+}
+
+template <bool F16, int ACT>
+int run_fwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const void* Wd, void* Y, char* ws, int64_t M,
+                int64_t C, int64_t F, int dtype, cudaStream_t st) {
+    const int sms = sm_count(dev);
+    if (sms <= 0 || encode_fn() == nullptr) return EVO_ERR_CUDA;
+    TrLayout L;
+    tr_layout(M, C, F, dtype, false, &L);
+    TrSource s = {X, nullptr, Wg, Wu, Wd, C, F};
+    if (L.pad && pad_weights(L, ws, &s, C, F, sms, st) != EVO_OK) return EVO_ERR_CUDA;
+    evo::TrMmaParams p = {};
+    p.C = int(C);
+    p.F = int(F);
+    p.h = reinterpret_cast<uint16_t*>(ws + L.h);
+    p.ldf = int(round_up(F, 128));
+    p.wide_store = wide_store(Y, C);
+    for (int64_t m = 0; m < M; m += L.chunk) {
+        p.rows = int(std::min(L.chunk, M - m));
+        const char* x = static_cast<const char*>(X) + m * C * 2;
+        if (L.pad) {
+            if (!pad_rows(x, ws + L.x, p.rows, C, s.ldc, sms, st)) return EVO_ERR_CUDA;
+            x = ws + L.x;
+        }
+        evo::TrMaps gate, out;
+        std::memset(&gate, 0, sizeof(gate));
+        std::memset(&out, 0, sizeof(out));
+        if (!encode_rows(&gate.m[0], x, p.rows, C, s.ldc, 128, F16) || !encode_rows(&gate.m[1], s.wg, F, C, s.ldc, 128, F16) ||
+            !encode_rows(&gate.m[2], s.wu, F, C, s.ldc, 128, F16) ||
+            !encode_rows(&out.m[0], p.h, p.rows, F, p.ldf, 128, F16) || !encode_rows(&out.m[1], s.wd, C, F, s.ldf, 128, F16))
+            return EVO_ERR_CUDA;
+        p.tiles_m = tiles_of(p.rows, 128);
+        p.tiles_n = tiles_of(F, 128);
+        p.num_tiles = p.tiles_m * p.tiles_n;
+        p.kb = tiles_of(C, 64);
+        if (launch_mma<evo::TR_GATE, ACT, F16, 256>(dev, sms, gate, p, st) != EVO_OK) return EVO_ERR_CUDA;
+        p.out = static_cast<uint16_t*>(Y) + m * C;
+        if (launch_out<evo::TR_OUT, F16>(dev, sms, out, p, st) != EVO_OK) return EVO_ERR_CUDA;
+    }
+    return EVO_OK;
+}
+
+template <bool F16, int ACT>
+int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const void* Wd, const void* dY, void* dX,
+                void* dWg, void* dWu, void* dWd, char* ws, int64_t M, int64_t C, int64_t F, int dtype, cudaStream_t st) {
+    using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
+    const int sms = sm_count(dev);
+    if (sms <= 0 || encode_fn() == nullptr) return EVO_ERR_CUDA;
+    TrLayout L;
+    tr_layout(M, C, F, dtype, true, &L);
+    TrSource s = {X, dY, Wg, Wu, Wd, C, F};
+    if (L.pad && pad_weights(L, ws, &s, C, F, sms, st) != EVO_OK) return EVO_ERR_CUDA;
+    evo::TrMmaParams p = {};
+    p.C = int(C);
+    p.F = int(F);
+    p.h = reinterpret_cast<uint16_t*>(ws + L.h);
+    p.dg = reinterpret_cast<uint16_t*>(ws + L.dg);
+    p.du = reinterpret_cast<uint16_t*>(ws + L.du);
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.ldf = int(round_up(F, 128));
+    p.ldc = int(round_up(C, 128));
+    p.ldf2 = int(round_up(F, 256));
+    p.split_rows = int(L.split_rows);
+    void* const dw[3] = {dWg, dWu, dWd};
+    for (int w = 0; w < 3; ++w)
+        if (dw[w]) p.which[p.num_which++] = w;
+    p.wide_store = dX ? wide_store(dX, C) : 0;
+    for (int64_t m = 0; m < M; m += L.chunk) {
+        p.rows = int(std::min(L.chunk, M - m));
+        p.first = m == 0;
+        const char* x = static_cast<const char*>(X) + m * C * 2;
+        const char* dy = static_cast<const char*>(dY) + m * C * 2;
+        if (L.pad) {
+            if (!pad_rows(x, ws + L.x, p.rows, C, s.ldc, sms, st) || !pad_rows(dy, ws + L.dy, p.rows, C, s.ldc, sms, st))
+                return EVO_ERR_CUDA;
+            x = ws + L.x;
+            dy = ws + L.dy;
+        }
+        evo::TrMaps grad, out, wgt;
+        std::memset(&out, 0, sizeof(out));
+        if (!encode_rows(&grad.m[0], x, p.rows, C, s.ldc, 128, F16) || !encode_rows(&grad.m[1], s.wg, F, C, s.ldc, 128, F16) ||
+            !encode_rows(&grad.m[2], s.wu, F, C, s.ldc, 128, F16) || !encode_rows(&grad.m[3], dy, p.rows, C, s.ldc, 128, F16) ||
+            !encode_rows(&grad.m[4], s.wd, C, F, s.ldf, 64, F16) ||
+            !encode_rows(&out.m[0], p.dg, p.rows, F, p.ldf, 128, F16) || !encode_rows(&out.m[1], s.wg, F, C, s.ldc, 64, F16) ||
+            !encode_rows(&out.m[2], p.du, p.rows, F, p.ldf, 128, F16) || !encode_rows(&out.m[3], s.wu, F, C, s.ldc, 64, F16) ||
+            !encode_rows(&wgt.m[0], x, p.rows, C, s.ldc, 64, F16) || !encode_rows(&wgt.m[1], dy, p.rows, C, s.ldc, 64, F16) ||
+            !encode_rows(&wgt.m[2], p.dg, p.rows, F, p.ldf, 64, F16) || !encode_rows(&wgt.m[3], p.du, p.rows, F, p.ldf, 64, F16) ||
+            !encode_rows(&wgt.m[4], p.h, p.rows, F, p.ldf, 64, F16))
+            return EVO_ERR_CUDA;
+        p.tiles_m = tiles_of(p.rows, 128);
+        p.tiles_n = tiles_of(F, 128);
+        p.num_tiles = p.tiles_m * p.tiles_n;
+        p.kb = tiles_of(C, 64);
+        if (launch_mma<evo::TR_GRAD, ACT, F16, 256>(dev, sms, grad, p, st) != EVO_OK) return EVO_ERR_CUDA;
+        if (dX) {
+            p.out = static_cast<uint16_t*>(dX) + m * C;
+            if (launch_out<evo::TR_DX, F16>(dev, sms, out, p, st) != EVO_OK) return EVO_ERR_CUDA;
+        }
+        if (p.num_which > 0) {
+            p.tiles_m = tiles_of(C, 128);
+            p.tiles_n = tiles_of(F, 256);
+            p.num_tiles = int(p.num_which * p.tiles_m * p.tiles_n * L.splits);
+            if (launch_mma<evo::TR_DW, 0, F16, 256>(dev, sms, wgt, p, st) != EVO_OK) return EVO_ERR_CUDA;
+        }
+    }
+    if (p.num_which > 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(blocks_of(F, 32), blocks_of(C, 32), 3);
+        cfg.blockDim = dim3(256, 1, 1);
+        cfg.stream = st;
+        if (cudaLaunchKernelEx(&cfg, evo::evo_tr_mma_reduce_kernel<T>, (const float*)p.part, int(L.splits), p.C, p.F, p.ldc,
+                               p.ldf2, static_cast<T*>(dWg), static_cast<T*>(dWu), static_cast<T*>(dWd)) != cudaSuccess)
+            return EVO_ERR_CUDA;
+    }
+    return EVO_OK;
+}
 
 int64_t tr_workspace(int64_t M, int64_t C, int64_t F, int dtype, bool backward) {
     const int st = check_transition(M, C, F, EVO_ACT_SILU, dtype);
@@ -279,8 +479,15 @@ extern "C" EVO_API int evo_transition_fwd(const void* X, const void* Wg, const v
     const int dev = select_device({X, Wg, Wu, Wd, Y, workspace}, scope);
     if (dev < 0) return dev;
     char* ws = static_cast<char*>(workspace);
-    EVO_TR_DISPATCH(run_fwd_simt, (static_cast<const T*>(X), static_cast<const T*>(Wg), static_cast<const T*>(Wu),
-                                   static_cast<const T*>(Wd), static_cast<T*>(Y), ws, M, C, F, dtype, st));
+    if (dtype == EVO_DTYPE_FP32) {
+        auto f = [](const void* p) { return static_cast<const float*>(p); };
+        auto run = act == EVO_ACT_SILU ? run_fwd_simt<EVO_ACT_SILU> : run_fwd_simt<EVO_ACT_GELU>;
+        return run(f(X), f(Wg), f(Wu), f(Wd), static_cast<float*>(Y), ws, M, C, F, dtype, st);
+    }
+    auto run = dtype == EVO_DTYPE_FP16
+                   ? (act == EVO_ACT_SILU ? run_fwd_mma<true, EVO_ACT_SILU> : run_fwd_mma<true, EVO_ACT_GELU>)
+                   : (act == EVO_ACT_SILU ? run_fwd_mma<false, EVO_ACT_SILU> : run_fwd_mma<false, EVO_ACT_GELU>);
+    return run(dev, X, Wg, Wu, Wd, Y, ws, M, C, F, dtype, st);
 }
 
 extern "C" EVO_API int evo_transition_bwd(const void* X, const void* Wg, const void* Wu, const void* Wd,
@@ -322,10 +529,16 @@ extern "C" EVO_API int evo_transition_bwd(const void* X, const void* Wg, const v
     const int dev = select_device({X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, workspace}, scope);
     if (dev < 0) return dev;
     char* ws = static_cast<char*>(workspace);
-    EVO_TR_DISPATCH(run_bwd_simt, (static_cast<const T*>(X), static_cast<const T*>(Wg), static_cast<const T*>(Wu),
-                                   static_cast<const T*>(Wd), static_cast<const T*>(dY), static_cast<T*>(dX),
-                                   static_cast<T*>(dWg), static_cast<T*>(dWu), static_cast<T*>(dWd), ws, M, C, F, dtype,
-                                   st));
+    if (dtype == EVO_DTYPE_FP32) {
+        auto f = [](const void* p) { return static_cast<const float*>(p); };
+        auto o = [](void* p) { return static_cast<float*>(p); };
+        auto run = act == EVO_ACT_SILU ? run_bwd_simt<EVO_ACT_SILU> : run_bwd_simt<EVO_ACT_GELU>;
+        return run(f(X), f(Wg), f(Wu), f(Wd), f(dY), o(dX), o(dWg), o(dWu), o(dWd), ws, M, C, F, dtype, st);
+    }
+    auto run = dtype == EVO_DTYPE_FP16
+                   ? (act == EVO_ACT_SILU ? run_bwd_mma<true, EVO_ACT_SILU> : run_bwd_mma<true, EVO_ACT_GELU>)
+                   : (act == EVO_ACT_SILU ? run_bwd_mma<false, EVO_ACT_SILU> : run_bwd_mma<false, EVO_ACT_GELU>);
+    return run(dev, X, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, ws, M, C, F, dtype, st);
 }
 
 // ------------------------------------------------- relative-position bias

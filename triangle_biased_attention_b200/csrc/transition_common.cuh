@@ -48,10 +48,6 @@ __device__ __forceinline__ void tr_act_grad(float g, float& a, float& da) {
     }
 }
 
-__device__ __forceinline__ float tr_load(const float* p) { return *p; }
-__device__ __forceinline__ float tr_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float tr_load(const __half* p) { return __half2float(*p); }
-__device__ __forceinline__ void tr_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void tr_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void tr_store(__half* p, float v) { *p = __float2half_rn(v); }
 

@@ -1,4 +1,5 @@
-// The transition's products on the FMA units, fp32 accumulation in registers.
+// The fp32 transition: products on the FMA units, sums in registers (1e-5 relative
+// accuracy rules out TF32).
 //
 // One tile routine serves every product: 256 threads hold a 128 x 128 tile of
 // fp32 sums, 8 x 8 a thread as two groups of four rows and of four columns 64
@@ -21,16 +22,14 @@ constexpr int kTrLd = 128 + 4;  // shared row of one k
 
 // One operand of a tile: element (row, k) of group h is p[h][row * ld + k] when
 // k is contiguous, p[h][k * ld + row] otherwise; rows >= lim[h] read as zero.
-template <typename T>
 struct TrOperand {
-    const T* p[2];
+    const float* p[2];
     int lim[2];
     long long ld;
 };
 
-template <typename T>
-__device__ __forceinline__ TrOperand<T> tr_rows(const T* p, long long row_stride, long long ld, int row0, int rows) {
-    TrOperand<T> o;
+__device__ __forceinline__ TrOperand tr_rows(const float* p, long long row_stride, long long ld, int row0, int rows) {
+    TrOperand o;
     o.ld = ld;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -42,24 +41,22 @@ __device__ __forceinline__ TrOperand<T> tr_rows(const T* p, long long row_stride
 
 // This thread's 8 elements of a 128 x 16 slab.  K-contiguous: 8 k of one row;
 // else 8 rows of one k.
-template <typename T, bool KC>
-__device__ __forceinline__ void tr_fetch(float (&v)[8], const TrOperand<T>& o, int k0, int kend, bool vec) {
+template <bool KC>
+__device__ __forceinline__ void tr_fetch(float (&v)[8], const TrOperand& o, int k0, int kend, bool vec) {
     const int t = threadIdx.x;
     const int row = KC ? (t >> 1) : (t & 15) * 8;
     const int k = k0 + (KC ? (t & 1) * 8 : (t >> 4));
     const int h = row >> 6, r = row & 63;
-    const T* p = KC ? o.p[h] + r * o.ld + k : o.p[h] + (long long)k * o.ld + r;
+    const float* p = KC ? o.p[h] + r * o.ld + k : o.p[h] + (long long)k * o.ld + r;
     const int n = KC ? (r < o.lim[h] ? kend - k : 0) : (k < kend ? o.lim[h] - r : 0);  // elements in range
-    if constexpr (sizeof(T) == 4) {
-        if (vec && n >= 8) {
-            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            return;
-        }
+    if (vec && n >= 8) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? tr_load(p + e) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
 }
 
 template <bool KC>
@@ -84,16 +81,16 @@ __device__ __forceinline__ void tr_fma2(float2& c, float2 a, float2 b) {
 
 // acc += A B^T over k in [kbeg, kend).  COLS: column groups computed (2, or 1
 // for a 64-column tile).  `smem` holds 4 slabs.
-template <typename T, bool AKC, bool BKC, int COLS>
-__device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOperand<T>& A, const TrOperand<T>& B,
+template <bool AKC, bool BKC, int COLS>
+__device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOperand& A, const TrOperand& B,
                                         int kbeg, int kend, bool vec, float* smem) {
     constexpr int SLAB = kTrK * kTrLd;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float va[8], vb[8];
     __syncthreads();  // an earlier product's slabs are no longer read
     if (kbeg < kend) {
-        tr_fetch<T, AKC>(va, A, kbeg, kend, vec);
-        tr_fetch<T, BKC>(vb, B, kbeg, kend, vec);
+        tr_fetch<AKC>(va, A, kbeg, kend, vec);
+        tr_fetch<BKC>(vb, B, kbeg, kend, vec);
         tr_put<AKC>(smem, va);
         tr_put<BKC>(smem + SLAB, vb);
     }
@@ -102,8 +99,8 @@ __device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOper
     for (int k0 = kbeg; k0 < kend; k0 += kTrK) {
         const bool more = k0 + kTrK < kend;
         if (more) {
-            tr_fetch<T, AKC>(va, A, k0 + kTrK, kend, vec);
-            tr_fetch<T, BKC>(vb, B, k0 + kTrK, kend, vec);
+            tr_fetch<AKC>(va, A, k0 + kTrK, kend, vec);
+            tr_fetch<BKC>(vb, B, k0 + kTrK, kend, vec);
         }
         const float* sa = smem + 2 * cur * SLAB;
         const float* sb = sa + SLAB;
@@ -142,24 +139,20 @@ __device__ __forceinline__ int tr_row(int i) {
 __device__ __forceinline__ int tr_col(int c, int e) { return 64 * c + 4 * int(threadIdx.x & 15) + e; }
 
 // Writes four consecutive columns of a row (n in range), 16 bytes at once where it may.
-template <typename T>
-__device__ __forceinline__ void tr_store4(T* p, const float (&v)[4], int n, bool vec) {
-    if constexpr (sizeof(T) == 4) {
-        if (vec && n >= 4) {
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            return;
-        }
+__device__ __forceinline__ void tr_store4(float* p, const float (&v)[4], int n, bool vec) {
+    if (vec && n >= 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        return;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (e < n) tr_store(p + e, v[e]);
+        if (e < n) p[e] = v[e];
 }
 
-template <typename T>
 struct TrSimtParams {
-    const T *x, *wg, *wu, *wd, *dy;
-    T *h, *dg, *du;        // [rows, F]
-    T* out;                // Y or dX, [rows, C]
+    const float *x, *wg, *wu, *wd, *dy;
+    float *h, *dg, *du;    // [rows, F]
+    float* out;                // Y or dX, [rows, C]
     float* part;           // [splits][3][F * C] partial weight gradients
     int rows, C, F;
     int splits, split_rows;
@@ -169,18 +162,18 @@ struct TrSimtParams {
 };
 
 // H = act(X Wg^T) * (X Wu^T): 128 rows x 64 features a block.
-template <typename T, int ACT>
-__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_gate_kernel(const TrSimtParams<T> p) {
+template <int ACT>
+__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_gate_kernel(const TrSimtParams p) {
     extern __shared__ __align__(16) float tr_smem[];
     const int f0 = blockIdx.x * 64, m0 = blockIdx.y * 128;
-    const TrOperand<T> A = tr_rows(p.x, p.C, p.C, m0, p.rows);
-    TrOperand<T> B;
+    const TrOperand A = tr_rows(p.x, p.C, p.C, m0, p.rows);
+    TrOperand B;
     B.ld = p.C;
     B.p[0] = p.wg + (long long)f0 * p.C;
     B.p[1] = p.wu + (long long)f0 * p.C;
     B.lim[0] = B.lim[1] = min(64, p.F - f0);
     float2 acc[8][4] = {};
-    tr_tile<T, true, true, 2>(acc, A, B, 0, p.C, p.vec, tr_smem);
+    tr_tile<true, true, 2>(acc, A, B, 0, p.C, p.vec, tr_smem);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int m = m0 + tr_row(i), f = f0 + tr_col(0, 0);
@@ -195,18 +188,18 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_gate_kernel(const TrSi
 }
 
 // Y = H Wd^T (BWD false), or dX = dG Wg + dU Wu: 128 rows x 128 channels a block.
-template <typename T, bool BWD>
-__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_out_kernel(const TrSimtParams<T> p) {
+template <bool BWD>
+__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_out_kernel(const TrSimtParams p) {
     extern __shared__ __align__(16) float tr_smem[];
     const int c0 = blockIdx.x * 128, m0 = blockIdx.y * 128;
     float2 acc[8][4] = {};
     if constexpr (BWD) {
-        tr_tile<T, true, false, 2>(acc, tr_rows(p.dg, p.F, p.F, m0, p.rows), tr_rows(p.wg, 1, p.C, c0, p.C), 0, p.F,
+        tr_tile<true, false, 2>(acc, tr_rows(p.dg, p.F, p.F, m0, p.rows), tr_rows(p.wg, 1, p.C, c0, p.C), 0, p.F,
                                    p.vec, tr_smem);
-        tr_tile<T, true, false, 2>(acc, tr_rows(p.du, p.F, p.F, m0, p.rows), tr_rows(p.wu, 1, p.C, c0, p.C), 0, p.F,
+        tr_tile<true, false, 2>(acc, tr_rows(p.du, p.F, p.F, m0, p.rows), tr_rows(p.wu, 1, p.C, c0, p.C), 0, p.F,
                                    p.vec, tr_smem);
     } else {
-        tr_tile<T, true, true, 2>(acc, tr_rows(p.h, p.F, p.F, m0, p.rows), tr_rows(p.wd, p.F, p.F, c0, p.C), 0, p.F,
+        tr_tile<true, true, 2>(acc, tr_rows(p.h, p.F, p.F, m0, p.rows), tr_rows(p.wd, p.F, p.F, c0, p.C), 0, p.F,
                                   p.vec, tr_smem);
     }
 #pragma unroll
@@ -224,21 +217,21 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_out_kernel(const TrSim
 
 // H, dG and dU from X and dY: the gate and up products are recomputed (no
 // [M, F] array of the forward is kept), then dH = dY Wd of the same 128 x 64 tile.
-template <typename T, int ACT>
-__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_grad_kernel(const TrSimtParams<T> p) {
+template <int ACT>
+__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_grad_kernel(const TrSimtParams p) {
     extern __shared__ __align__(16) float tr_smem[];
     const int f0 = blockIdx.x * 64, m0 = blockIdx.y * 128;
-    TrOperand<T> B;
+    TrOperand B;
     B.ld = p.C;
     B.p[0] = p.wg + (long long)f0 * p.C;
     B.p[1] = p.wu + (long long)f0 * p.C;
     B.lim[0] = B.lim[1] = min(64, p.F - f0);
     float2 acc[8][4] = {};
-    tr_tile<T, true, true, 2>(acc, tr_rows(p.x, p.C, p.C, m0, p.rows), B, 0, p.C, p.vec, tr_smem);
+    tr_tile<true, true, 2>(acc, tr_rows(p.x, p.C, p.C, m0, p.rows), B, 0, p.C, p.vec, tr_smem);
     float2 dh[8][2] = {};
-    TrOperand<T> D = tr_rows(p.wd, 1, p.F, f0, p.F);
+    TrOperand D = tr_rows(p.wd, 1, p.F, f0, p.F);
     D.lim[1] = 0;
-    tr_tile<T, true, false, 1>(dh, tr_rows(p.dy, p.C, p.C, m0, p.rows), D, 0, p.C, p.vec, tr_smem);
+    tr_tile<true, false, 1>(dh, tr_rows(p.dy, p.C, p.C, m0, p.rows), D, 0, p.C, p.vec, tr_smem);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int m = m0 + tr_row(i), f = f0 + tr_col(0, 0);
@@ -265,8 +258,7 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_grad_kernel(const TrSi
 // Partial weight gradients of one range of rows: dG^T X, dU^T X [F, C] and
 // dY^T H [C, F], summed into this range's own slot (chunks of rows run one after
 // another, so each slot is added to in a fixed order: no atomics).
-template <typename T>
-__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_dw_kernel(const TrSimtParams<T> p) {
+static __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_dw_kernel(const TrSimtParams p) {
     extern __shared__ __align__(16) float tr_smem[];
     const int which = blockIdx.z % 3, split = blockIdx.z / 3;
     if (!((p.dw_mask >> which) & 1)) return;
@@ -274,10 +266,10 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_dw_kernel(const TrSimt
     const int r0 = blockIdx.y * 128, n0 = blockIdx.x * 128;
     if (r0 >= R || n0 >= N) return;
     const int m_beg = split * p.split_rows, m_end = min(p.rows, m_beg + p.split_rows);
-    const T* a = which == 0 ? p.dg : which == 1 ? p.du : p.dy;
-    const T* b = which == 2 ? p.h : p.x;
+    const float* a = which == 0 ? p.dg : which == 1 ? p.du : p.dy;
+    const float* b = which == 2 ? p.h : p.x;
     float2 acc[8][4] = {};
-    tr_tile<T, false, false, 2>(acc, tr_rows(a, 1, R, r0, R), tr_rows(b, 1, N, n0, N), m_beg, m_end, p.vec, tr_smem);
+    tr_tile<false, false, 2>(acc, tr_rows(a, 1, R, r0, R), tr_rows(b, 1, N, n0, N), m_beg, m_end, p.vec, tr_smem);
     float* out = p.part + ((long long)split * 3 + which) * p.F * p.C;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -298,19 +290,18 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_dw_kernel(const TrSimt
     }
 }
 
-// dW = the sum of its slots in order, rounded to the type.
-template <typename T>
-__global__ void __launch_bounds__(256) evo_tr_dw_reduce_kernel(const float* __restrict__ part, int splits, long long n,
-                                                               T* dwg, T* dwu, T* dwd) {
+// dW = the sum of its slots in order.
+static __global__ void __launch_bounds__(256) evo_tr_dw_reduce_kernel(const float* __restrict__ part, int splits,
+                                                                      long long n, float* dwg, float* dwu, float* dwd) {
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
-    T* const out[3] = {dwg, dwu, dwd};
+    float* const out[3] = {dwg, dwu, dwd};
 #pragma unroll
     for (int w = 0; w < 3; ++w) {
         if (out[w] == nullptr) continue;
         float s = 0.0f;
         for (int k = 0; k < splits; ++k) s += part[((long long)k * 3 + w) * n + i];
-        tr_store(out[w] + i, s);
+        out[w][i] = s;
     }
 }
 

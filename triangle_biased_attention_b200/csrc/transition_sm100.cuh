@@ -1,0 +1,514 @@
+// The transition's products on the tensor cores (bf16 / fp16 operands, fp32
+// accumulation in tensor memory), for sm_100a.
+//
+// Rows are taken in chunks whose [rows, F] intermediates stay in L2.  Five
+// products, one persistent kernel template (a CTA per SM, tiles with a stride of
+// the grid):
+//   GATE  H = act(X Wg^T) * (X Wu^T)     128 rows x 128 features: the rows of Wg
+//         and Wu for the same features are one 256-row operand, so both
+//         projections are one N = 256 MMA per 16-deep step, and a thread of the
+//         epilogue finds G and U of its elements in the same tensor-memory lane.
+//   OUT   Y = H Wd^T                     128 rows x BN channels
+//   GRAD  dH = dY Wd beside G and U; writes H, dG, dU.  Tensor memory holds G and
+//         U once (256 columns) and dH twice, so that the next tile's dH product
+//         runs during this tile's epilogue.
+//   DX    dX = dG Wg + dU Wu             128 rows x BN channels, both products
+//         into one accumulator
+//   DW    [X^T dG, X^T dU, dY^T H], [C, F] each: 128 channels x 256 features of
+//         one range of rows, summed into the range's own fp32 slot.
+// Operands that are contiguous along k are read K-major, the others (Wd in GRAD,
+// the weights in DX, both in DW) MN-major: the same swizzled TMA boxes of 128-byte
+// rows serve both, so nothing is transposed in memory.
+//
+// Warp roles (384 threads): warp 0 loads (TMA ring), warp 1 issues the MMAs,
+// warps 4-11 drain the accumulators: warp w reads the 32 tensor-memory lanes of
+// its place in its warpgroup, the two warpgroups half the columns each.  Stores
+// go straight from registers, 32 whole bytes a thread.
+// Every wait is bounded (2 s); on expiry the CTA records EVO_ERR_TIMEOUT, drains
+// its own copies and MMAs, frees tensor memory and exits.
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+
+#include "tile_sm100.cuh"
+#include "transition_common.cuh"
+
+namespace evo {
+
+enum TrKind { TR_GATE, TR_OUT, TR_GRAD, TR_DX, TR_DW };
+
+// GATE: X, Wg, Wu.  OUT: H, Wd.  GRAD: X, Wg, Wu, dY, Wd.  DX: dG, Wg, dU, Wu.
+// DW: X, dY, dG, dU, H.
+struct TrMaps {
+    CUtensorMap m[5];
+};
+
+struct TrMmaParams {
+    uint16_t *h, *dg, *du;  // [rows up to 128, ldf]
+    uint16_t* out;          // Y or dX, [rows, C]
+    float* part;            // DW: [splits][3][ldc][ldf2]
+    int rows, C, F;
+    int ldf;                // row stride of h, dg, du: F rounded up to 128
+    int ldc, ldf2;          // rows and row stride of a slot: C up to 128, F up to 256
+    int tiles_m, tiles_n, num_tiles;
+    int kb;                 // 64-deep K blocks of one product
+    int split_rows;         // DW: rows of a range, a multiple of 64
+    int which[3], num_which;  // DW: the gradients asked for
+    int first;              // DW: the slots start here
+    int wide_store;         // OUT, DX: 2 = 32-byte stores, 1 = 16-byte, 0 = single elements
+};
+
+template <int KIND, int BN, bool F16>
+struct TrCfg {
+    static constexpr int THREADS = 384;
+    static constexpr int STAGES = 4;
+    static constexpr int OPER_A = 128 * 128;   // 128 rows x 64 k, or 64 k x 128 columns
+    static constexpr int OPER_B = BN * 128;
+    static constexpr int STAGE_BYTES = OPER_A + OPER_B;
+    static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+    static constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_AF = 2 * STAGES, BAR_AE = 2 * STAGES + 2,
+                         BAR_DRAIN = 2 * STAGES + 4, NUM_BARS = 2 * STAGES + 5;
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static constexpr uint32_t TMEM_COLS = KIND == TR_GRAD ? 512 : 2 * BN;
+    static constexpr uint32_t AB = F16 ? 0u : ((1u << 7) | (1u << 10));
+    __host__ __device__ static constexpr uint32_t idesc(bool a_mn, bool b_mn, int n) {
+        return (1u << 4) | AB | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t(n) >> 3) << 17) |
+               ((128u >> 4) << 24);
+    }
+};
+
+// act(g) * u for two elements.  One reciprocal serves both sigmoids:
+// 1/a = b / (a b), which leaves the special-function unit 1.5 instructions an
+// element instead of 2.  The exponent is held at 2^60 so that a b stays finite:
+// below g = -41 the result is then at most 2^-60 |g u| instead of e^g |g u|.
+__device__ __forceinline__ void tr_sigmoid2(float g0, float g1, float& s0, float& s1) {
+    const float a = 1.0f + ptx::ex2_approx(fminf(-kLog2e * g0, 60.0f));
+    const float b = 1.0f + ptx::ex2_approx(fminf(-kLog2e * g1, 60.0f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+    s0 = r * b;
+    s1 = r * a;
+}
+
+// Phi(g) and e^(-g^2/2): the complementary error function by Abramowitz and
+// Stegun's formula 7.1.26 (absolute error at most 1.5e-7, below the rounding of
+// a 16-bit result and of the same size as the fp32 error of g itself).
+__device__ __forceinline__ float tr_phi(float g, float& e) {
+    const float x = fabsf(g) * 0.70710678118654752f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    e = ptx::ex2_approx(-kLog2e * x * x);
+    const float half = 0.5f * p * t * e;  // Phi(-|g|)
+    return g >= 0.0f ? 1.0f - half : half;
+}
+
+// h = act(g) * u of a pair
+template <int ACT>
+__device__ __forceinline__ void tr_gate2(const float* g, const float* u, float* h) {
+    if constexpr (ACT == EVO_ACT_SILU) {
+        float s0, s1;
+        tr_sigmoid2(g[0], g[1], s0, s1);
+        h[0] = g[0] * u[0] * s0;
+        h[1] = g[1] * u[1] * s1;
+    } else {
+        float e;
+        h[0] = g[0] * u[0] * tr_phi(g[0], e);
+        h[1] = g[1] * u[1] * tr_phi(g[1], e);
+    }
+}
+
+// h, dg and du of a pair from g, u and d = dH
+template <int ACT>
+__device__ __forceinline__ void tr_grad2(const float* g, const float* u, const float* d, float* h, float* dg,
+                                         float* du) {
+    float p[2], e[2];
+    if constexpr (ACT == EVO_ACT_SILU) {
+        tr_sigmoid2(g[0], g[1], p[0], p[1]);
+    } else {
+        p[0] = tr_phi(g[0], e[0]);
+        p[1] = tr_phi(g[1], e[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float a = g[i] * p[i];
+        float da;
+        if constexpr (ACT == EVO_ACT_SILU) da = fmaf(a, 1.0f - p[i], p[i]);
+        else da = fmaf(g[i] * 0.3989422804014327f, e[i], p[i]);
+        h[i] = a * u[i];
+        du[i] = d[i] * a;
+        dg[i] = d[i] * u[i] * da;
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t tr_pack(float lo, float hi) {
+    return F16 ? ptx::pack_f16x2(lo, hi) : ptx::pack_bf16x2(lo, hi);
+}
+
+// Eight words (16 elements) to 32-byte aligned global memory in one store.
+__device__ __forceinline__ void tr_st_global_x8(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+template <int KIND, int ACT, bool F16, int BN>
+__global__ void __launch_bounds__(384, 1)
+evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
+    using C = TrCfg<KIND, BN, F16>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = ptx::smem_u32(smem);
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    const int G = gridDim.x;
+    auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8u * uint32_t(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+    // K blocks of one tile; GRAD runs dH's product first, then G and U; DX dG's, then dU's
+    constexpr int PRODUCTS = (KIND == TR_GRAD || KIND == TR_DX) ? 2 : 1;
+    // tile L: column block fastest.  DW: gradient, then column and row block, then range of rows
+    auto tile = [&](int L, int& tn, int& tm, int& which, int& split) {
+        which = split = 0;
+        if constexpr (KIND == TR_DW) {
+            which = p.which[L % p.num_which];
+            L /= p.num_which;
+        }
+        tn = L % p.tiles_n;
+        L /= p.tiles_n;
+        tm = L % p.tiles_m;
+        split = L / p.tiles_m;
+    };
+    auto blocks = [&](int split) -> int {
+        if constexpr (KIND == TR_DW) {
+            const int n = min(p.split_rows, p.rows - split * p.split_rows);
+            return n > 0 ? (n + 63) / 64 : 0;
+        }
+        return p.kb;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            ptx::mbar_init(bar(C::BAR_FULL + s), 1);
+            ptx::mbar_init(bar(C::BAR_EMPTY + s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(bar(C::BAR_AF + a), 1);
+            ptx::mbar_init(bar(C::BAR_AE + a), 8);
+        }
+        ptx::mbar_init(bar(C::BAR_DRAIN), 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- loads
+        int n = 0;
+        bool ok = true;
+        for (int L = blockIdx.x; L < p.num_tiles && ok; L += G) {
+            int tn, tm, which, split;
+            tile(L, tn, tm, which, split);
+            const int kbs = blocks(split);
+#pragma unroll 1
+            for (int kt = 0; kt < PRODUCTS * kbs; ++kt, ++n) {
+                const int s = n % C::STAGES;
+                ok = wait_warp(bar(C::BAR_EMPTY + s), ((n / C::STAGES) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t a = sb + uint32_t(s * C::STAGE_BYTES), b = a + C::OPER_A;
+                    const uint32_t f = bar(C::BAR_FULL + s);
+                    const bool second = PRODUCTS == 2 && kt >= kbs;
+                    const int k = 64 * (second ? kt - kbs : kt);
+                    if constexpr (KIND == TR_GATE) {
+                        ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
+                        ptx::tma_load_2d(a, &maps.m[0], f, k, 128 * tm);
+                        ptx::tma_load_2d(b, &maps.m[1], f, k, 128 * tn);
+                        ptx::tma_load_2d(b + 16384, &maps.m[2], f, k, 128 * tn);
+                    } else if constexpr (KIND == TR_GRAD) {
+                        if (!second) {
+                            ptx::mbar_arrive_expect_tx(f, C::OPER_A + 16384);
+                            ptx::tma_load_2d(a, &maps.m[3], f, k, 128 * tm);
+                            ptx::tma_load_2d(b, &maps.m[4], f, 128 * tn, k);
+                            ptx::tma_load_2d(b + 8192, &maps.m[4], f, 128 * tn + 64, k);
+                        } else {
+                            ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
+                            ptx::tma_load_2d(a, &maps.m[0], f, k, 128 * tm);
+                            ptx::tma_load_2d(b, &maps.m[1], f, k, 128 * tn);
+                            ptx::tma_load_2d(b + 16384, &maps.m[2], f, k, 128 * tn);
+                        }
+                    } else if constexpr (KIND == TR_OUT) {
+                        ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
+                        ptx::tma_load_2d(a, &maps.m[0], f, k, 128 * tm);
+#pragma unroll
+                        for (int x = 0; x < BN / 128; ++x)
+                            ptx::tma_load_2d(b + 16384 * x, &maps.m[1], f, k, BN * tn + 128 * x);
+                    } else if constexpr (KIND == TR_DX) {
+                        ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
+                        ptx::tma_load_2d(a, &maps.m[second ? 2 : 0], f, k, 128 * tm);
+#pragma unroll
+                        for (int x = 0; x < BN / 64; ++x)
+                            ptx::tma_load_2d(b + 8192 * x, &maps.m[second ? 3 : 1], f, BN * tn + 64 * x, k);
+                    } else {
+                        const int m = split * p.split_rows + k;
+                        ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            ptx::tma_load_2d(a + 8192 * x, &maps.m[which == 2 ? 1 : 0], f, 128 * tm + 64 * x, m);
+#pragma unroll
+                        for (int x = 0; x < BN / 64; ++x)
+                            ptx::tma_load_2d(b + 8192 * x, &maps.m[2 + which], f, BN * tn + 64 * x, m);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) {
+            // the last load of each stage lands before the CTA exits
+            for (int s = 0; s < C::STAGES; ++s)
+                if (n - 1 >= s) {
+                    const int last = s + C::STAGES * ((n - 1 - s) / C::STAGES);
+                    wait_bounded(bar(C::BAR_FULL + s), uint32_t(last / C::STAGES) & 1u, nullptr);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // --------------------------------------------------------------- MMAs
+        int n = 0, t = 0;
+        bool ok = true, issued = false;
+        for (int L = blockIdx.x; L < p.num_tiles && ok; L += G, ++t) {
+            int tn, tm, which, split;
+            tile(L, tn, tm, which, split);
+            const int kbs = blocks(split), acc = t & 1;
+            // the epilogue has drained this accumulator's previous tile
+            ok = wait_warp(bar(C::BAR_AE + acc), ((t >> 1) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int kt = 0; kt < PRODUCTS * kbs; ++kt, ++n) {
+                const int s = n % C::STAGES;
+                const bool second = PRODUCTS == 2 && kt >= kbs;
+                if (KIND == TR_GRAD && kt == kbs && t > 0) {
+                    // G and U share one place: the previous tile's epilogue is done with them
+                    ok = wait_warp(bar(C::BAR_AE + (acc ^ 1)), uint32_t((t - 1) >> 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                }
+                ok = wait_warp(bar(C::BAR_FULL + s), uint32_t(n / C::STAGES) & 1u, abort_flag);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t a = sb + uint32_t(s * C::STAGE_BYTES), b = a + C::OPER_A;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if constexpr (KIND == TR_GRAD) {
+                        const uint32_t add = ((second ? kt - kbs : kt) > 0 || kk > 0) ? 1u : 0u;
+                        if (!second)
+                            ptx::mma_ss_elect(tmem + uint32_t(256 + 128 * acc), desc_k_major<128>(a + 32 * kk),
+                                              desc_mn_major<128>(b + 2048 * kk, 8192), C::idesc(false, true, 128), add);
+                        else
+                            ptx::mma_ss_elect(tmem, desc_k_major<128>(a + 32 * kk), desc_k_major<128>(b + 32 * kk),
+                                              C::idesc(false, false, 256), add);
+                    } else {
+                        constexpr bool A_MN = KIND == TR_DW, B_MN = KIND == TR_DW || KIND == TR_DX;
+                        const uint64_t da = A_MN ? desc_mn_major<128>(a + 2048 * kk, 8192) : desc_k_major<128>(a + 32 * kk);
+                        const uint64_t db = B_MN ? desc_mn_major<128>(b + 2048 * kk, 8192) : desc_k_major<128>(b + 32 * kk);
+                        ptx::mma_ss_elect(tmem + uint32_t(BN * acc), da, db, C::idesc(A_MN, B_MN, BN),
+                                          (kt > 0 || kk > 0) ? 1u : 0u);
+                    }
+                }
+                issued = true;
+                ptx::mma_commit_elect(bar(C::BAR_EMPTY + s));
+            }
+            if (!ok) break;
+            ptx::mma_commit_elect(bar(C::BAR_AF + acc));
+        }
+        if (!ok && issued) {
+            ptx::mma_commit_elect(bar(C::BAR_DRAIN));
+            wait_bounded(bar(C::BAR_DRAIN), 0, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ----------------------------------------------------------- epilogue
+        const int wq = warp & 3, half = (warp - 4) >> 2;
+        const int r = 32 * wq + lane;
+        const uint32_t tl = tmem + (uint32_t(32 * wq) << 16);
+        int t = 0;
+        bool ok = true;
+        for (int L = blockIdx.x; L < p.num_tiles && ok; L += G, ++t) {
+            int tn, tm, which, split;
+            tile(L, tn, tm, which, split);
+            const int acc = t & 1;
+            ok = wait_warp(bar(C::BAR_AF + acc), uint32_t(t >> 1) & 1u, abort_flag);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            auto release = [&]() {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive_elect(bar(C::BAR_AE + acc));
+            };
+            if constexpr (KIND == TR_GATE) {
+                // rows past `rows` and features past F are zero (their operands read as zero)
+                uint16_t* row = p.h + size_t(128 * tm + r) * p.ldf + 128 * tn + 64 * half;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    float g[32], u[32];
+                    ptx::tmem_ld_x32(tl + uint32_t(256 * acc + 64 * half + 32 * c), reinterpret_cast<uint32_t*>(g));
+                    ptx::tmem_ld_x32(tl + uint32_t(256 * acc + 128 + 64 * half + 32 * c), reinterpret_cast<uint32_t*>(u));
+                    ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
+                    ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
+                    if (c == 1) release();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float h[2];
+                        tr_gate2<ACT>(g + 2 * e, u + 2 * e, h);
+                        w[e] = tr_pack<F16>(h[0], h[1]);
+                    }
+                    tr_st_global_x8(row + 32 * c, w);
+                    tr_st_global_x8(row + 32 * c + 16, w + 8);
+                }
+            } else if constexpr (KIND == TR_GRAD) {
+                const size_t at = size_t(128 * tm + r) * p.ldf + 128 * tn + 64 * half;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float g[16], u[16], d[16];
+                    ptx::tmem_ld_x16(tl + uint32_t(64 * half + 16 * c), reinterpret_cast<uint32_t*>(g));
+                    ptx::tmem_ld_x16(tl + uint32_t(128 + 64 * half + 16 * c), reinterpret_cast<uint32_t*>(u));
+                    ptx::tmem_ld_x16(tl + uint32_t(256 + 128 * acc + 64 * half + 16 * c), reinterpret_cast<uint32_t*>(d));
+                    ptx::tmem_ld_wait_x16(reinterpret_cast<uint32_t*>(g));
+                    ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(u));
+                    ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(u) + 8);
+                    ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(d));
+                    ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(d) + 8);
+                    if (c == 3) release();
+                    uint32_t wh[8], wg[8], wu[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float h[2], dg[2], du[2];
+                        tr_grad2<ACT>(g + 2 * e, u + 2 * e, d + 2 * e, h, dg, du);
+                        wh[e] = tr_pack<F16>(h[0], h[1]);
+                        wg[e] = tr_pack<F16>(dg[0], dg[1]);
+                        wu[e] = tr_pack<F16>(du[0], du[1]);
+                    }
+                    tr_st_global_x8(p.h + at + 16 * c, wh);
+                    tr_st_global_x8(p.dg + at + 16 * c, wg);
+                    tr_st_global_x8(p.du + at + 16 * c, wu);
+                }
+            } else if constexpr (KIND == TR_DW) {
+                const int cols = BN / 2;
+                float* row = p.part + ((size_t(split) * 3 + which) * p.ldc + 128 * tm + r) * p.ldf2 + BN * tn + cols * half;
+                const bool empty = blocks(split) == 0;  // a range past the chunk's rows adds nothing
+#pragma unroll 1
+                for (int c = 0; c < cols / 32; ++c) {
+                    float v[32];
+                    ptx::tmem_ld_x32(tl + uint32_t(BN * acc + cols * half + 32 * c), reinterpret_cast<uint32_t*>(v));
+                    ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
+                    if (c == cols / 32 - 1) release();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float4* o = reinterpret_cast<float4*>(row + 32 * c + 4 * e);
+                        float4 x = empty ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                         : make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        if (!p.first) {
+                            const float4 y = *o;
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        *o = x;
+                    }
+                }
+            } else {
+                const int cols = BN / 2, m = 128 * tm + r;
+                uint16_t* row = p.out + size_t(m) * p.C;
+#pragma unroll 1
+                for (int c = 0; c < cols / 32; ++c) {
+                    float v[32];
+                    ptx::tmem_ld_x32(tl + uint32_t(BN * acc + cols * half + 32 * c), reinterpret_cast<uint32_t*>(v));
+                    ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
+                    if (c == cols / 32 - 1) release();
+                    const int c0 = BN * tn + cols * half + 32 * c;
+                    if (m < p.rows) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = tr_pack<F16>(v[2 * e], v[2 * e + 1]);
+                        if (p.wide_store == 2) {
+                            if (c0 < p.C) tr_st_global_x8(row + c0, w);
+                            if (c0 + 16 < p.C) tr_st_global_x8(row + c0 + 16, w + 8);
+                        } else if (p.wide_store == 1) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (c0 + 8 * e < p.C)
+                                    *reinterpret_cast<uint4*>(row + c0 + 8 * e) =
+                                        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (c0 + e < p.C) row[c0 + e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// Rows of `w` elements copied to rows of `wp` (w rounded up to 8): TMA reads rows
+// of whole 16-byte units only.  What lies behind column w is never read.
+static __global__ void __launch_bounds__(256) evo_tr_pad_kernel(const uint16_t* __restrict__ x, uint16_t* __restrict__ y,
+                                                                long long rows, int w, int wp) {
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < rows * w; i += (long long)gridDim.x * blockDim.x) {
+        const long long r = i / w;
+        y[r * wp + (i - r * w)] = x[i];
+    }
+}
+
+// The weight gradients from their slots, added in order and rounded to the type:
+// slot 0 and 1 hold dWg and dWu as [C, F] and are written transposed, slot 2 holds dWd.
+template <typename T>
+__global__ void __launch_bounds__(256) evo_tr_mma_reduce_kernel(const float* __restrict__ part, int splits, int C, int F,
+                                                                int ldc, int ldf2, T* dwg, T* dwu, T* dwd) {
+    __shared__ float tile[32][33];
+    const int which = blockIdx.z;
+    T* out = which == 0 ? dwg : which == 1 ? dwu : dwd;
+    if (out == nullptr) return;
+    const int f0 = blockIdx.x * 32, c0 = blockIdx.y * 32, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const size_t slot = size_t(ldc) * ldf2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = c0 + ty + 8 * i, f = f0 + tx;  // inside the padded slot
+        float s = 0.0f;
+        for (int k = 0; k < splits; ++k) s += part[(size_t(k) * 3 + which) * slot + size_t(c) * ldf2 + f];
+        if (which == 2) {
+            if (c < C && f < F) tr_store(out + size_t(c) * F + f, s);
+        } else {
+            tile[ty + 8 * i][tx] = s;
+        }
+    }
+    if (which == 2) return;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int f = f0 + ty + 8 * i, c = c0 + tx;
+        if (c < C && f < F) tr_store(out + size_t(f) * C + c, tile[tx][ty + 8 * i]);
+    }
+}
+
+}  // namespace evo
