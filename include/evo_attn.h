@@ -364,9 +364,9 @@ EVO_API int64_t evo_transition_bwd_workspace_size(int64_t M, int64_t C, int64_t 
  *   Wd         [C, F] of `dtype`.
  *   Y          [M, C] of `dtype`, written.
  *   workspace  device scratch of at least evo_transition_fwd_workspace_size
- *              bytes, 256-byte aligned, owned by the caller, overwritten; two
- *              calls (or captured graphs) that may run at the same time need
- *              one each.
+ *              bytes (NULL where that is 0), 256-byte aligned, owned by the
+ *              caller, overwritten; two calls (or captured graphs) that may run
+ *              at the same time need one each.
  *   M, C, F    >= 0.  No row or no channel is a no-op, no feature (F = 0) gives
  *              Y = 0.
  *   act        an evo_act_t.  dtype: an evo_dtype_t.

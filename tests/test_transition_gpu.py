@@ -68,6 +68,22 @@ def test_more_rows_than_one_chunk():
     check(*make(M, C, F, BF16, seed=1), "silu", f"chunks {M}")
 
 
+@pytest.mark.parametrize("shape,dt", [((8321, 128, 512), BF16), ((8200, 40, 72), FP16), ((19100, 256, 304), BF16),
+                                      ((20001, 192, 136), FP16), ((8193, 100, 130), BF16), ((38000, 64, 128), BF16),
+                                      ((9000, 250, 400), FP16), ((8193, 1, 1), BF16)], ids=str)
+def test_many_rows_of_few_channels(shape, dt):
+    """Sizes at which Y of a row tile is formed without the [M, F] array: one and
+    several tiles a CTA, one and several feature chunks, C up to 128 and up to 256."""
+    M, C, F = shape
+    act = "gelu" if M % 2 else "silu"
+    x, wg, wu, wd, _ = make(M, C, F, dt, seed=M)
+    y = evo.transition(x, wg, wu, wd, act=act)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    ref, err = T.forward(x, wg, wu, wd, act, dt)
+    within(y, ref, err, f"{shape} {dt}")
+    assert torch.equal(evo.transition(x, wg, wu, wd, act=act), y)
+
+
 def test_activation_range():
     """Gates far out on both sides: no overflow on the way to 0 or to g."""
     gates = torch.tensor([-1e30, -3e4, -100.0, -88.5, -87.0, -20.0, -1.0, -0.0, 1e-30, 20.0, 100.0, 1e3])

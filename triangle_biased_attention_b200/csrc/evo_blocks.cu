@@ -86,10 +86,15 @@ struct TrLayout {
     int64_t h = 0, dg = 0, du = 0;                // [chunk, F] (16-bit: rows up to 128, F up to 128)
     int64_t part = 0;                             // partial weight gradients, fp32
     int64_t splits = 0, split_rows = 0;           // ranges of rows with a slot of their own
+    bool fused = false;                           // the forward's one-kernel form: no [M, F] array at all
     int64_t x = 0, dy = 0, wg = 0, wu = 0, wd = 0;  // 16-bit, odd C or F: copies with rows of whole 16-byte units
     bool pad = false;
     int64_t total = 0;
 };
+
+// The one-kernel forward holds Y of 128 rows in tensor memory (C <= 256) and
+// gives a tile of rows to one SM, so it wants tiles for most of them.
+bool tr_fused(int64_t M, int64_t C, int dtype) { return dtype != EVO_DTYPE_FP32 && C <= 256 && M > 64 * 128; }
 
 // Sections on 256-byte boundaries.  False when a byte count passes int64.
 bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayout* L) {
@@ -97,7 +102,11 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
     // C, F <= 2^20 and M < 2^31 (check_transition): the products below fit
     const int64_t fc = F * C;
     const int64_t ldf = dtype == EVO_DTYPE_FP32 ? F : round_up(F, 128);
-    L->chunk = tr_chunk_rows(M, ldf * es * (backward ? 3 : 1));
+    L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
+    L->fused = !backward && tr_fused(M, C, dtype);
+    // (the one-kernel forward needs chunks only for the copy of X)
+    L->chunk = L->fused ? (L->pad ? tr_chunk_rows(M, round_up(C, 8) * 2) : M)
+                        : tr_chunk_rows(M, ldf * es * (backward ? 3 : 1));
     const int64_t hbytes = (dtype == EVO_DTYPE_FP32 ? L->chunk : round_up(L->chunk, 128)) * ldf * es;
     int64_t off = 0;
     auto take = [&off](int64_t bytes) {
@@ -105,7 +114,7 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
         off += round_up(bytes, 256);
         return at;
     };
-    L->h = take(hbytes);
+    if (!L->fused) L->h = take(hbytes);
     if (backward) {
         L->dg = take(hbytes);
         L->du = take(hbytes);
@@ -123,7 +132,6 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
             L->part = take(L->splits * 3 * round_up(C, 128) * round_up(F, 256) * 4);
         }
     }
-    L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
     if (L->pad) {
         const int64_t cp = round_up(C, 8), fp = round_up(F, 8);
         L->x = take(L->chunk * cp * 2);
@@ -304,6 +312,35 @@ int launch_out(int dev, int sms, const evo::TrMaps& maps, evo::TrMmaParams p, cu
                      : launch_mma<KIND, 0, F16, 128>(dev, sms, maps, p, st);
 }
 
+template <int ACT, bool F16, int CN>
+int launch_fused(int dev, int sms, const void* x, const TrSource& s, uint16_t* y, int rows, int64_t C, int64_t F, int wide,
+                 cudaStream_t st) {
+    using Cfg = evo::TrFusedCfg<F16, CN>;
+    auto kernel = evo::evo_tr_fused_kernel<ACT, F16, CN>;
+    static AttrOnce attr;
+    if (!attr.ensure(dev, kernel, Cfg::SMEM_BYTES)) return EVO_ERR_CUDA;
+    evo::TrMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (!encode_rows(&maps.m[0], x, rows, C, s.ldc, 128, F16) || !encode_rows(&maps.m[1], s.wg, F, C, s.ldc, 128, F16) ||
+        !encode_rows(&maps.m[2], s.wu, F, C, s.ldc, 128, F16) || !encode_rows(&maps.m[3], s.wd, C, F, s.ldf, 128, F16))
+        return EVO_ERR_CUDA;
+    evo::TrFusedParams p = {};
+    p.out = y;
+    p.M = rows;
+    p.C = int(C);
+    p.F = int(F);
+    p.num_tiles = tiles_of(rows, 128);
+    p.kc = tiles_of(C, 64);
+    p.chunks = tiles_of(F, 128);
+    p.wide_store = wide;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min(p.num_tiles, sms)), 1, 1);
+    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p) == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
 template <bool F16, int ACT>
 int run_fwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const void* Wd, void* Y, char* ws, int64_t M,
                 int64_t C, int64_t F, int dtype, cudaStream_t st) {
@@ -325,6 +362,14 @@ int run_fwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
         if (L.pad) {
             if (!pad_rows(x, ws + L.x, p.rows, C, s.ldc, sms, st)) return EVO_ERR_CUDA;
             x = ws + L.x;
+        }
+        if (L.fused) {
+            const int fst = C > 128 ? launch_fused<ACT, F16, 256>(dev, sms, x, s, static_cast<uint16_t*>(Y) + m * C, p.rows,
+                                                                  C, F, p.wide_store, st)
+                                    : launch_fused<ACT, F16, 128>(dev, sms, x, s, static_cast<uint16_t*>(Y) + m * C, p.rows,
+                                                                  C, F, p.wide_store, st);
+            if (fst != EVO_OK) return fst;
+            continue;
         }
         evo::TrMaps gate, out;
         std::memset(&gate, 0, sizeof(gate));
@@ -457,12 +502,13 @@ extern "C" EVO_API int evo_transition_fwd(const void* X, const void* Wg, const v
     if (M == 0 || C == 0) return EVO_OK;  // Y is empty
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int64_t es = elem_bytes(dtype);
-    if (!Y || (F > 0 && (!X || !Wg || !Wu || !Wd || !workspace))) return EVO_ERR_INVALID_ARG;
+    if (!Y || (F > 0 && (!X || !Wg || !Wu || !Wd))) return EVO_ERR_INVALID_ARG;
     TrLayout L;
     if (F > 0 && !tr_layout(M, C, F, dtype, false, &L)) return EVO_ERR_UNSUPPORTED_SHAPE;
     const int64_t xb = M * C * es, wb = F * C * es;
     if (F > 0) {
-        if (workspace_bytes < L.total) return EVO_ERR_INVALID_ARG;
+        if (workspace_bytes < L.total || (!workspace && L.total > 0)) return EVO_ERR_INVALID_ARG;
+        if (L.total == 0) workspace = nullptr;  // not used
         for (const void* p : {X, Wg, Wu, Wd, static_cast<const void*>(Y)})
             if (!aligned(p, tr_alignment(C, F, dtype))) return EVO_ERR_MISALIGNED;
         if (!aligned(workspace, 256)) return EVO_ERR_MISALIGNED;

@@ -80,17 +80,32 @@ struct TrCfg {
     }
 };
 
-// act(g) * u for two elements.  One reciprocal serves both sigmoids:
-// 1/a = b / (a b), which leaves the special-function unit 1.5 instructions an
-// element instead of 2.  The exponent is held at 2^60 so that a b stays finite:
-// below g = -41 the result is then at most 2^-60 |g u| instead of e^g |g u|.
-__device__ __forceinline__ void tr_sigmoid2(float g0, float g1, float& s0, float& s1) {
-    const float a = 1.0f + ptx::ex2_approx(fminf(-kLog2e * g0, 60.0f));
-    const float b = 1.0f + ptx::ex2_approx(fminf(-kLog2e * g1, 60.0f));
+__device__ __forceinline__ float2 tr_mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 tr_add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+    return d;
+}
+
+// sigmoid of two elements.  One reciprocal serves both: 1/a = b / (a b), which
+// leaves the special-function unit 1.5 instructions an element instead of 2.
+// The exponent is held at 2^60 so that a b stays finite: below g = -41 the
+// result is 2^-60 instead of e^g, both nothing beside the rounding of g u.
+__device__ __forceinline__ float2 tr_sigmoid2(float2 g) {
+    const float2 x = tr_mul2(g, make_float2(-kLog2e, -kLog2e));
+    const float2 e = make_float2(ptx::ex2_approx(fminf(x.x, 60.0f)), ptx::ex2_approx(fminf(x.y, 60.0f)));
+    const float2 a = tr_add2(e, make_float2(1.0f, 1.0f));
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-    s0 = r * b;
-    s1 = r * a;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a.x * a.y));
+    return tr_mul2(make_float2(r, r), make_float2(a.y, a.x));
 }
 
 // Phi(g) and e^(-g^2/2): the complementary error function by Abramowitz and
@@ -110,40 +125,35 @@ __device__ __forceinline__ float tr_phi(float g, float& e) {
 
 // h = act(g) * u of a pair
 template <int ACT>
-__device__ __forceinline__ void tr_gate2(const float* g, const float* u, float* h) {
+__device__ __forceinline__ float2 tr_gate2(float2 g, float2 u) {
+    const float2 gu = tr_mul2(g, u);
     if constexpr (ACT == EVO_ACT_SILU) {
-        float s0, s1;
-        tr_sigmoid2(g[0], g[1], s0, s1);
-        h[0] = g[0] * u[0] * s0;
-        h[1] = g[1] * u[1] * s1;
+        return tr_mul2(gu, tr_sigmoid2(g));
     } else {
         float e;
-        h[0] = g[0] * u[0] * tr_phi(g[0], e);
-        h[1] = g[1] * u[1] * tr_phi(g[1], e);
+        return make_float2(gu.x * tr_phi(g.x, e), gu.y * tr_phi(g.y, e));
     }
 }
 
 // h, dg and du of a pair from g, u and d = dH
 template <int ACT>
-__device__ __forceinline__ void tr_grad2(const float* g, const float* u, const float* d, float* h, float* dg,
-                                         float* du) {
-    float p[2], e[2];
+__device__ __forceinline__ void tr_grad2(float2 g, float2 u, float2 d, float2& h, float2& dg, float2& du) {
+    float2 p, e;
     if constexpr (ACT == EVO_ACT_SILU) {
-        tr_sigmoid2(g[0], g[1], p[0], p[1]);
+        p = tr_sigmoid2(g);
     } else {
-        p[0] = tr_phi(g[0], e[0]);
-        p[1] = tr_phi(g[1], e[1]);
+        p.x = tr_phi(g.x, e.x);
+        p.y = tr_phi(g.y, e.y);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float a = g[i] * p[i];
-        float da;
-        if constexpr (ACT == EVO_ACT_SILU) da = fmaf(a, 1.0f - p[i], p[i]);
-        else da = fmaf(g[i] * 0.3989422804014327f, e[i], p[i]);
-        h[i] = a * u[i];
-        du[i] = d[i] * a;
-        dg[i] = d[i] * u[i] * da;
-    }
+    const float2 a = tr_mul2(g, p);
+    float2 da;
+    if constexpr (ACT == EVO_ACT_SILU)
+        da = make_float2(fmaf(a.x, 1.0f - p.x, p.x), fmaf(a.y, 1.0f - p.y, p.y));
+    else
+        da = make_float2(fmaf(g.x * 0.3989422804014327f, e.x, p.x), fmaf(g.y * 0.3989422804014327f, e.y, p.y));
+    h = tr_mul2(a, u);
+    du = tr_mul2(d, a);
+    dg = tr_mul2(tr_mul2(d, u), da);
 }
 
 template <bool F16>
@@ -156,6 +166,27 @@ __device__ __forceinline__ void tr_st_global_x8(void* p, const uint32_t* w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
+}
+
+// 32 columns c0 .. c0 + 31 of an output row of C columns.
+template <bool F16>
+__device__ __forceinline__ void tr_store_row(uint16_t* row, int c0, int C, int wide, const float* v) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = tr_pack<F16>(v[2 * e], v[2 * e + 1]);
+    if (wide == 2) {
+        if (c0 < C) tr_st_global_x8(row + c0, w);
+        if (c0 + 16 < C) tr_st_global_x8(row + c0 + 16, w + 8);
+    } else if (wide == 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c0 + 8 * e < C)
+                *reinterpret_cast<uint4*>(row + c0 + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (c0 + e < C) row[c0 + e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+    }
 }
 
 template <int KIND, int ACT, bool F16, int BN>
@@ -373,9 +404,9 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        float h[2];
-                        tr_gate2<ACT>(g + 2 * e, u + 2 * e, h);
-                        w[e] = tr_pack<F16>(h[0], h[1]);
+                        const float2 h = tr_gate2<ACT>(make_float2(g[2 * e], g[2 * e + 1]),
+                                                       make_float2(u[2 * e], u[2 * e + 1]));
+                        w[e] = tr_pack<F16>(h.x, h.y);
                     }
                     tr_st_global_x8(row + 32 * c, w);
                     tr_st_global_x8(row + 32 * c + 16, w + 8);
@@ -397,11 +428,12 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     uint32_t wh[8], wg[8], wu[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        float h[2], dg[2], du[2];
-                        tr_grad2<ACT>(g + 2 * e, u + 2 * e, d + 2 * e, h, dg, du);
-                        wh[e] = tr_pack<F16>(h[0], h[1]);
-                        wg[e] = tr_pack<F16>(dg[0], dg[1]);
-                        wu[e] = tr_pack<F16>(du[0], du[1]);
+                        float2 h, dg, du;
+                        tr_grad2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]),
+                                      make_float2(d[2 * e], d[2 * e + 1]), h, dg, du);
+                        wh[e] = tr_pack<F16>(h.x, h.y);
+                        wg[e] = tr_pack<F16>(dg.x, dg.y);
+                        wu[e] = tr_pack<F16>(du.x, du.y);
                     }
                     tr_st_global_x8(p.h + at + 16 * c, wh);
                     tr_st_global_x8(p.dg + at + 16 * c, wg);
@@ -439,29 +471,308 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
                     if (c == cols / 32 - 1) release();
                     const int c0 = BN * tn + cols * half + 32 * c;
-                    if (m < p.rows) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = tr_pack<F16>(v[2 * e], v[2 * e + 1]);
-                        if (p.wide_store == 2) {
-                            if (c0 < p.C) tr_st_global_x8(row + c0, w);
-                            if (c0 + 16 < p.C) tr_st_global_x8(row + c0 + 16, w + 8);
-                        } else if (p.wide_store == 1) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (c0 + 8 * e < p.C)
-                                    *reinterpret_cast<uint4*>(row + c0 + 8 * e) =
-                                        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (c0 + e < p.C) row[c0 + e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
-                        }
-                    }
+                    if (m < p.rows) tr_store_row<F16>(row, c0, p.C, p.wide_store, v);
                     __syncwarp();
                 }
             }
         }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// ------------------------------------------------------- the whole block at once
+
+// Y of 128 rows in one CTA, for C <= 256: the rows' X stays in shared memory, the
+// weights stream through a ring (from L2, where they stay), H never leaves the
+// SM.  Per chunk of 128 features: G and U (one N = 256 MMA a step) into 256
+// columns of tensor memory; the epilogue warps turn them into a 128 x 128 tile
+// of H in shared memory (double-buffered, swizzled as the tensor core reads it);
+// Y += H Wd^T accumulates in CN columns of tensor memory.  The MMA warp issues
+// GU(q + 1) before OUT(q), across tiles too, so that a chunk's activation runs
+// beside the next chunk's products; a tile's Y is drained after the first
+// activation of the next tile.
+struct TrFusedParams {
+    uint16_t* out;  // Y [M, C]
+    int M, C, F;
+    int num_tiles;  // ceil(M / 128)
+    int kc;         // 64-deep blocks of C
+    int chunks;     // ceil(F / 128)
+    int wide_store;
+};
+
+template <bool F16, int CN>
+struct TrFusedCfg {
+    static constexpr int THREADS = 384;
+    static constexpr int XSLOTS = 4;               // 128 rows x 64 k of X, 16 KB each
+    static constexpr int STAGES = 3;               // weights: 32 KB each
+    static constexpr int OUT_STAGES = CN / 128;    // ring stages of Wd for a chunk
+    static constexpr int OFF_H = XSLOTS * 16384;   // two tiles of 128 rows x 128 features
+    static constexpr int OFF_W = OFF_H + 2 * 32768;
+    static constexpr int OFF_BAR = OFF_W + STAGES * 32768;
+    static constexpr int XF = 0, XE = XF + XSLOTS, WF = XE + XSLOTS, WE = WF + STAGES, GF = WE + STAGES, GE = GF + 1,
+                         HF = GE + 1, HE = HF + 2, OF = HE + 2, OE = OF + 1, DRAIN = OE + 1, NUM_BARS = DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static constexpr uint32_t TMEM_COLS = 512;     // G, U: 0-255, Y: 256 - 256 + CN - 1
+    static constexpr uint32_t AB = F16 ? 0u : ((1u << 7) | (1u << 10));
+    __host__ __device__ static constexpr uint32_t idesc(int n) {
+        return (1u << 4) | AB | ((uint32_t(n) >> 3) << 17) | ((128u >> 4) << 24);
+    }
+};
+
+// maps: X, Wg, Wu, Wd
+template <int ACT, bool F16, int CN>
+__global__ void __launch_bounds__(384, 1)
+evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) {
+    using C = TrFusedCfg<F16, CN>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = ptx::smem_u32(smem);
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    const int G = gridDim.x;
+    auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8u * uint32_t(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    const int my_tiles = (p.num_tiles - int(blockIdx.x) + G - 1) / G;
+    const int total = my_tiles * p.chunks;  // this CTA's chunks, in order
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::XSLOTS; ++i) {
+            ptx::mbar_init(bar(C::XF + i), 1);
+            ptx::mbar_init(bar(C::XE + i), 1);
+        }
+        for (int i = 0; i < C::STAGES; ++i) {
+            ptx::mbar_init(bar(C::WF + i), 1);
+            ptx::mbar_init(bar(C::WE + i), 1);
+        }
+        ptx::mbar_init(bar(C::GF), 1);
+        ptx::mbar_init(bar(C::GE), 8);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(C::HF + i), 8);
+            ptx::mbar_init(bar(C::HE + i), 1);
+        }
+        ptx::mbar_init(bar(C::OF), 1);
+        ptx::mbar_init(bar(C::OE), 8);
+        ptx::mbar_init(bar(C::DRAIN), 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- loads
+        int n = 0, xn = 0;  // weight stages and X slots filled so far
+        bool ok = true;
+        auto weights = [&](bool gate, int chunk, int k) -> bool {
+            const int s = n % C::STAGES;
+            if (!wait_warp(bar(C::WE + s), ((n / C::STAGES) & 1) ^ 1, abort_flag)) return false;
+            if (lane == 0) {
+                const uint32_t d = sb + uint32_t(C::OFF_W + 32768 * s), f = bar(C::WF + s);
+                ptx::mbar_arrive_expect_tx(f, 32768);
+                if (gate) {
+                    ptx::tma_load_2d(d, &maps.m[1], f, 64 * k, 128 * chunk);
+                    ptx::tma_load_2d(d + 16384, &maps.m[2], f, 64 * k, 128 * chunk);
+                } else if (CN == 128) {  // 128 channels x both halves of the chunk's features
+                    ptx::tma_load_2d(d, &maps.m[3], f, 128 * chunk, 0);
+                    ptx::tma_load_2d(d + 16384, &maps.m[3], f, 128 * chunk + 64, 0);
+                } else {                 // 256 channels x half k of the chunk's features
+                    ptx::tma_load_2d(d, &maps.m[3], f, 128 * chunk + 64 * k, 0);
+                    ptx::tma_load_2d(d + 16384, &maps.m[3], f, 128 * chunk + 64 * k, 128);
+                }
+            }
+            __syncwarp();
+            ++n;
+            return true;
+        };
+        int tile = blockIdx.x, j = 0, prev = 0;
+        for (int q = 0; q <= total && ok; ++q) {
+            if (q < total) {
+                if (j == 0) {
+                    for (int k = 0; k < p.kc && ok; ++k, ++xn) {
+                        const int s = xn % C::XSLOTS;
+                        ok = wait_warp(bar(C::XE + s), ((xn / C::XSLOTS) & 1) ^ 1, abort_flag);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            ptx::mbar_arrive_expect_tx(bar(C::XF + s), 16384);
+                            ptx::tma_load_2d(sb + uint32_t(16384 * s), &maps.m[0], bar(C::XF + s), 64 * k, 128 * tile);
+                        }
+                        __syncwarp();
+                    }
+                }
+                for (int k = 0; k < p.kc && ok; ++k) ok = weights(true, j, k);
+            }
+            if (q > 0)
+                for (int k = 0; k < C::OUT_STAGES && ok; ++k) ok = weights(false, prev, k);
+            prev = j;
+            if (++j == p.chunks) {
+                j = 0;
+                tile += G;
+            }
+        }
+        if (!ok && lane == 0) {
+            // the last load of each slot and stage lands before the CTA exits
+            for (int s = 0; s < C::STAGES; ++s)
+                if (n - 1 >= s) wait_bounded(bar(C::WF + s), uint32_t((n - 1 - s) / C::STAGES) & 1u, nullptr);
+            for (int s = 0; s < C::XSLOTS; ++s)
+                if (xn - 1 >= s) wait_bounded(bar(C::XF + s), uint32_t((xn - 1 - s) / C::XSLOTS) & 1u, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // --------------------------------------------------------------- MMAs
+        int n = 0, xfirst = 0, t = 0;  // stages used, first X slot of the tile, tile count
+        bool ok = true, issued = false;
+        int j = 0;
+        for (int q = 0; q <= total && ok; ++q) {
+            if (q < total) {
+                // G and U of chunk q, once the activation of chunk q - 1 has read its own
+                ok = wait_warp(bar(C::GE), (q & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                for (int k = 0; k < p.kc; ++k, ++n) {
+                    const int s = n % C::STAGES, x = (xfirst + k) % C::XSLOTS;
+                    if (j == 0) ok = wait_warp(bar(C::XF + x), uint32_t((xfirst + k) / C::XSLOTS) & 1u, abort_flag);
+                    if (!ok) break;
+                    ok = wait_warp(bar(C::WF + s), uint32_t(n / C::STAGES) & 1u, abort_flag);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t a = sb + uint32_t(16384 * x), b = sb + uint32_t(C::OFF_W + 32768 * s);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_ss_elect(tmem, desc_k_major<128>(a + 32 * kk), desc_k_major<128>(b + 32 * kk),
+                                          C::idesc(256), (k > 0 || kk > 0) ? 1u : 0u);
+                    issued = true;
+                    ptx::mma_commit_elect(bar(C::WE + s));
+                    if (j == p.chunks - 1) ptx::mma_commit_elect(bar(C::XE + x));
+                }
+                if (!ok) break;
+                ptx::mma_commit_elect(bar(C::GF));
+            }
+            if (q > 0) {
+                // Y += H(q - 1) Wd^T
+                const int qo = q - 1, jo = j > 0 ? j - 1 : p.chunks - 1, hb = qo & 1;
+                if (jo == 0) {  // the first chunk of tile t: the tile before it has been drained
+                    ok = wait_warp(bar(C::OE), (t & 1) ^ 1, abort_flag);
+                    if (!ok) break;
+                }
+                ok = wait_warp(bar(C::HF + hb), uint32_t(qo >> 1) & 1u, abort_flag);
+                if (!ok) break;
+                for (int k = 0; k < C::OUT_STAGES; ++k, ++n) {
+                    const int s = n % C::STAGES;
+                    ok = wait_warp(bar(C::WF + s), uint32_t(n / C::STAGES) & 1u, abort_flag);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t h = sb + uint32_t(C::OFF_H + 32768 * hb), b = sb + uint32_t(C::OFF_W + 32768 * s);
+#pragma unroll
+                    for (int kk = 0; kk < 8 / C::OUT_STAGES; ++kk) {
+                        const int f = kk + 4 * k;  // 16-feature step of the chunk
+                        ptx::mma_ss_elect(tmem + 256u, desc_k_major<128>(h + 16384 * (f >> 2) + 32 * (f & 3)),
+                                          desc_k_major<128>(b + (CN == 128 ? 16384 * (f >> 2) : 0) + 32 * (f & 3)),
+                                          C::idesc(CN), (jo > 0 || f > 0) ? 1u : 0u);
+                    }
+                    issued = true;
+                    ptx::mma_commit_elect(bar(C::WE + s));
+                }
+                if (!ok) break;
+                ptx::mma_commit_elect(bar(C::HE + hb));
+                if (jo == p.chunks - 1) {
+                    ptx::mma_commit_elect(bar(C::OF));
+                    ++t;
+                }
+            }
+            if (++j == p.chunks) {
+                j = 0;
+                xfirst += p.kc;
+            }
+        }
+        if (!ok && issued) {
+            ptx::mma_commit_elect(bar(C::DRAIN));
+            wait_bounded(bar(C::DRAIN), 0, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ----------------------------------------------------------- epilogue
+        const int wq = warp & 3, half = (warp - 4) >> 2;
+        const int r = 32 * wq + lane;
+        const uint32_t tl = tmem + (uint32_t(32 * wq) << 16);
+        bool ok = true;
+        int tile = blockIdx.x, j = 0, t = 0;
+        auto drain = [&](int of_tile) -> bool {
+            if (!wait_warp(bar(C::OF), uint32_t(t) & 1u, abort_flag)) return false;
+            ptx::tc_fence_after();
+            const int m = 128 * of_tile + r;
+            uint16_t* row = p.out + size_t(m) * p.C;
+#pragma unroll 1
+            for (int c = 0; c < CN / 64; ++c) {
+                float v[32];
+                const int c0 = CN / 2 * half + 32 * c;
+                ptx::tmem_ld_x32(tl + uint32_t(256 + c0), reinterpret_cast<uint32_t*>(v));
+                ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
+                if (c == CN / 64 - 1) {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive_elect(bar(C::OE));
+                }
+                if (m < p.M) tr_store_row<F16>(row, c0, p.C, p.wide_store, v);
+                __syncwarp();
+            }
+            ++t;
+            return true;
+        };
+        for (int q = 0; q < total && ok; ++q) {
+            ok = wait_warp(bar(C::GF), uint32_t(q) & 1u, abort_flag);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t h = sb + uint32_t(C::OFF_H + 32768 * (q & 1) + 16384 * half);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                float g[32], u[32];
+                ptx::tmem_ld_x32(tl + uint32_t(64 * half + 32 * c), reinterpret_cast<uint32_t*>(g));
+                ptx::tmem_ld_x32(tl + uint32_t(128 + 64 * half + 32 * c), reinterpret_cast<uint32_t*>(u));
+                ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
+                ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
+                if (c == 1) {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive_elect(bar(C::GE));
+                }
+                if (c == 0) {  // the product that read this H tile last is done
+                    ok = wait_warp(bar(C::HE + (q & 1)), uint32_t((q >> 1) & 1) ^ 1u, abort_flag);
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int o = 8 * e + 2 * i;
+                        const float2 hv = tr_gate2<ACT>(make_float2(g[o], g[o + 1]), make_float2(u[o], u[o + 1]));
+                        w[i] = tr_pack<F16>(hv.x, hv.y);
+                    }
+                    ptx::st_shared_v4(h + swz_chunk<128>(r, 4 * c + e), make_uint4(w[0], w[1], w[2], w[3]));
+                }
+            }
+            if (!ok) break;
+            ptx::fence_proxy_async_smem();  // H is read by the tensor cores
+            __syncwarp();
+            ptx::mbar_arrive_elect(bar(C::HF + (q & 1)));
+            if (j == 0 && q > 0) ok = drain(tile - G);
+            if (++j == p.chunks) {
+                j = 0;
+                tile += G;
+            }
+        }
+        if (ok && total > 0) drain(tile - G);
     }
 
     ptx::tc_fence_before();
