@@ -84,6 +84,21 @@ def test_many_rows_of_few_channels(shape, dt):
     assert torch.equal(evo.transition(x, wg, wu, wd, act=act), y)
 
 
+@pytest.mark.parametrize("C,F", [(256, 1024), (192, 512), (128, 512), (64, 256)])
+def test_msa_size(C, F):
+    """Long runs of chunks in every CTA (131072 rows, the MSA of 512 sequences of 256
+    residues): sampled rows against the oracle, repeated calls to the bit."""
+    x, wg, wu, wd, _ = make(512 * 256, C, F, BF16, seed=C)
+    y = evo.transition(x, wg, wu, wd)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    at = torch.arange(0, 512 * 256, 251)
+    ref, err = T.forward(x[at], wg, wu, wd, "silu", BF16)
+    within(y[at], ref, err, f"{C} {F}")
+    for _ in range(5):
+        assert torch.equal(evo.transition(x, wg, wu, wd), y)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+
+
 def test_activation_range():
     """Gates far out on both sides: no overflow on the way to 0 or to g."""
     gates = torch.tensor([-1e30, -3e4, -100.0, -88.5, -87.0, -20.0, -1.0, -0.0, 1e-30, 20.0, 100.0, 1e3])

@@ -238,17 +238,18 @@ int run_bwd_simt(const float* X, const float* Wg, const float* Wu, const float* 
     return EVO_OK;
 }
 
-// A 16-bit matrix of `rows` rows of `cols` elements, `ld` apart; a box is 64
-// columns (128 B rows, 128 B swizzle) of `box_rows` rows.
-bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f16) {
+// A 16-bit matrix of `rows` rows of `cols` elements, `ld` apart; a box is 64 (or
+// 32) columns of `box_rows` rows, swizzled over its 128 B (64 B) rows.
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f16,
+                 int box_cols = 64) {
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(ld * 2)};
-    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
     return encode_fn()(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                       box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // One product over one chunk of rows, a CTA per SM.
@@ -322,7 +323,8 @@ int launch_fused(int dev, int sms, const void* x, const TrSource& s, uint16_t* y
     evo::TrMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     if (!encode_rows(&maps.m[0], x, rows, C, s.ldc, 128, F16) || !encode_rows(&maps.m[1], s.wg, F, C, s.ldc, 128, F16) ||
-        !encode_rows(&maps.m[2], s.wu, F, C, s.ldc, 128, F16) || !encode_rows(&maps.m[3], s.wd, C, F, s.ldf, 128, F16))
+        !encode_rows(&maps.m[2], s.wu, F, C, s.ldc, 128, F16) || !encode_rows(&maps.m[3], s.wd, C, F, s.ldf, 128, F16) ||
+        (wide && !encode_rows(&maps.m[4], y, rows, C, C, 32, F16, 32)))
         return EVO_ERR_CUDA;
     evo::TrFusedParams p = {};
     p.out = y;

@@ -490,31 +490,39 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
 // weights stream through a ring (from L2, where they stay), H never leaves the
 // SM.  Per chunk of 128 features: G and U (one N = 256 MMA a step) into 256
 // columns of tensor memory; the epilogue warps turn them into a 128 x 128 tile
-// of H in shared memory (double-buffered, swizzled as the tensor core reads it);
-// Y += H Wd^T accumulates in CN columns of tensor memory.  The MMA warp issues
-// GU(q + 1) before OUT(q), across tiles too, so that a chunk's activation runs
-// beside the next chunk's products; a tile's Y is drained after the first
-// activation of the next tile.
+// of H in shared memory (swizzled as the tensor core reads it); Y += H Wd^T
+// accumulates in CN columns of tensor memory.  One warp issues the products GU,
+// another OUT (an issuing warp is busy for most of an MMA's time, so one would
+// leave the tensor cores idle at its waits); GU(q + 1) runs beside the activation
+// of chunk q, across tiles too, and a tile's Y is drained after the first
+// activation of the next tile.  An activation holds its packed H in registers
+// until OUT of the chunk before has read the one H tile.  Y goes through 32 x 32
+// tiles a warp of shared memory and TMA stores: straight from registers, a warp's
+// 32-byte pieces of 32 rows held up the H stores of the other warps (a drain took
+// 2000 cycles of a tile's 12000 at C = 128).
 struct TrFusedParams {
     uint16_t* out;  // Y [M, C]
     int M, C, F;
     int num_tiles;  // ceil(M / 128)
     int kc;         // 64-deep blocks of C
     int chunks;     // ceil(F / 128)
-    int wide_store;
+    int wide_store;  // Y through TMA (rows of whole 16-byte units), else element by element
 };
 
 template <bool F16, int CN>
 struct TrFusedCfg {
-    static constexpr int THREADS = 384;
+    static constexpr int EPI_WARPS = 16;           // a warp: 32 rows x 32 features of a chunk
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int XSLOTS = 4;               // 128 rows x 64 k of X, 16 KB each
     static constexpr int STAGES = 3;               // weights: 32 KB each
     static constexpr int OUT_STAGES = CN / 128;    // ring stages of Wd for a chunk
-    static constexpr int OFF_H = XSLOTS * 16384;   // two tiles of 128 rows x 128 features
-    static constexpr int OFF_W = OFF_H + 2 * 32768;
+    static constexpr int OFF_H = XSLOTS * 16384;   // 128 rows x 128 features
+    static constexpr int OFF_Y = OFF_H + 32768;    // 2 KB a warp: 32 rows x 32 channels of Y
+    static constexpr int OFF_W = OFF_Y + EPI_WARPS * 2048;
     static constexpr int OFF_BAR = OFF_W + STAGES * 32768;
     static constexpr int XF = 0, XE = XF + XSLOTS, WF = XE + XSLOTS, WE = WF + STAGES, GF = WE + STAGES, GE = GF + 1,
-                         HF = GE + 1, HE = HF + 2, OF = HE + 2, OE = OF + 1, DRAIN = OE + 1, NUM_BARS = DRAIN + 1;
+                         HF = GE + 1, HE = HF + 1, OF = HE + 1, OE = OF + 1, GC = OE + 1, OC = GC + 1, DRAIN = OC + 1,
+                         NUM_BARS = DRAIN + 2;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -525,9 +533,9 @@ struct TrFusedCfg {
     }
 };
 
-// maps: X, Wg, Wu, Wd
+// maps: X, Wg, Wu, Wd, Y
 template <int ACT, bool F16, int CN>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
 evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) {
     using C = TrFusedCfg<F16, CN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -552,14 +560,15 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
             ptx::mbar_init(bar(C::WE + i), 1);
         }
         ptx::mbar_init(bar(C::GF), 1);
-        ptx::mbar_init(bar(C::GE), 8);
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(bar(C::HF + i), 8);
-            ptx::mbar_init(bar(C::HE + i), 1);
-        }
+        ptx::mbar_init(bar(C::GE), C::EPI_WARPS);
+        ptx::mbar_init(bar(C::HF), C::EPI_WARPS);
+        ptx::mbar_init(bar(C::HE), 1);
         ptx::mbar_init(bar(C::OF), 1);
-        ptx::mbar_init(bar(C::OE), 8);
+        ptx::mbar_init(bar(C::OE), C::EPI_WARPS);
+        ptx::mbar_init(bar(C::GC), 1);
+        ptx::mbar_init(bar(C::OC), 1);
         ptx::mbar_init(bar(C::DRAIN), 1);
+        ptx::mbar_init(bar(C::DRAIN + 1), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -571,6 +580,15 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // Fill n of the weight ring has landed.  Two warps take stages from the one
+    // ring.  A parity cannot tell fill n of a stage from the one two fills before,
+    // so a warp must know that the fill between, which may be the other warp's, has
+    // landed: GU(q) starts when OUT(q - 2) has seen its stages land (barrier OC),
+    // OUT(q) when GU(q + 1) has (GC).  Every stage before GU(q) and OUT(q) in the
+    // ring's order is one of those, an earlier one or the warp's own.
+    auto weights_full = [&](int n) -> bool {
+        return wait_warp(bar(C::WF + n % C::STAGES), uint32_t(n / C::STAGES) & 1u, abort_flag);
+    };
 
     if (warp == 0) {
         // -------------------------------------------------------------- loads
@@ -631,70 +649,42 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
         }
         __syncwarp();
     } else if (warp == 1) {
-        // --------------------------------------------------------------- MMAs
-        int n = 0, xfirst = 0, t = 0;  // stages used, first X slot of the tile, tile count
+        // ---------------------------------------------------------- GU products
+        // weight stages come in the order GU(0), GU(1), OUT(0), GU(2), OUT(1), ...
+        int j = 0, xn = 0;
         bool ok = true, issued = false;
-        int j = 0;
-        for (int q = 0; q <= total && ok; ++q) {
-            if (q < total) {
-                // G and U of chunk q, once the activation of chunk q - 1 has read its own
-                ok = wait_warp(bar(C::GE), (q & 1) ^ 1, abort_flag);
+        for (int q = 0; q < total && ok; ++q) {
+            // the activation of chunk q - 1 has read its G and U
+            ok = wait_warp(bar(C::GE), (q & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (q >= 2) {
+                ok = wait_warp(bar(C::OC), uint32_t(q) & 1u, abort_flag);  // OUT(q - 2)
                 if (!ok) break;
+            }
+            const int n0 = q * p.kc + max(q - 1, 0) * C::OUT_STAGES;
+            for (int k = 0; k < p.kc; ++k) {
+                const int n = n0 + k, s = n % C::STAGES, x = (xn + k) % C::XSLOTS;
+                if (j == 0) ok = wait_warp(bar(C::XF + x), uint32_t((xn + k) / C::XSLOTS) & 1u, abort_flag);
+                if (!ok) break;
+                ok = weights_full(n);
+                if (!ok) break;
+                if (k == p.kc - 1) ptx::mbar_arrive_elect(bar(C::GC));
                 ptx::tc_fence_after();
-                for (int k = 0; k < p.kc; ++k, ++n) {
-                    const int s = n % C::STAGES, x = (xfirst + k) % C::XSLOTS;
-                    if (j == 0) ok = wait_warp(bar(C::XF + x), uint32_t((xfirst + k) / C::XSLOTS) & 1u, abort_flag);
-                    if (!ok) break;
-                    ok = wait_warp(bar(C::WF + s), uint32_t(n / C::STAGES) & 1u, abort_flag);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t a = sb + uint32_t(16384 * x), b = sb + uint32_t(C::OFF_W + 32768 * s);
+                const uint32_t a = sb + uint32_t(16384 * x), b = sb + uint32_t(C::OFF_W + 32768 * s);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_ss_elect(tmem, desc_k_major<128>(a + 32 * kk), desc_k_major<128>(b + 32 * kk),
-                                          C::idesc(256), (k > 0 || kk > 0) ? 1u : 0u);
-                    issued = true;
-                    ptx::mma_commit_elect(bar(C::WE + s));
-                    if (j == p.chunks - 1) ptx::mma_commit_elect(bar(C::XE + x));
-                }
-                if (!ok) break;
-                ptx::mma_commit_elect(bar(C::GF));
+                for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_ss_elect(tmem, desc_k_major<128>(a + 32 * kk), desc_k_major<128>(b + 32 * kk), C::idesc(256),
+                                      (k > 0 || kk > 0) ? 1u : 0u);
+                issued = true;
+                ptx::mma_commit_elect(bar(C::WE + s));
+                if (j == p.chunks - 1) ptx::mma_commit_elect(bar(C::XE + x));
             }
-            if (q > 0) {
-                // Y += H(q - 1) Wd^T
-                const int qo = q - 1, jo = j > 0 ? j - 1 : p.chunks - 1, hb = qo & 1;
-                if (jo == 0) {  // the first chunk of tile t: the tile before it has been drained
-                    ok = wait_warp(bar(C::OE), (t & 1) ^ 1, abort_flag);
-                    if (!ok) break;
-                }
-                ok = wait_warp(bar(C::HF + hb), uint32_t(qo >> 1) & 1u, abort_flag);
-                if (!ok) break;
-                for (int k = 0; k < C::OUT_STAGES; ++k, ++n) {
-                    const int s = n % C::STAGES;
-                    ok = wait_warp(bar(C::WF + s), uint32_t(n / C::STAGES) & 1u, abort_flag);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t h = sb + uint32_t(C::OFF_H + 32768 * hb), b = sb + uint32_t(C::OFF_W + 32768 * s);
-#pragma unroll
-                    for (int kk = 0; kk < 8 / C::OUT_STAGES; ++kk) {
-                        const int f = kk + 4 * k;  // 16-feature step of the chunk
-                        ptx::mma_ss_elect(tmem + 256u, desc_k_major<128>(h + 16384 * (f >> 2) + 32 * (f & 3)),
-                                          desc_k_major<128>(b + (CN == 128 ? 16384 * (f >> 2) : 0) + 32 * (f & 3)),
-                                          C::idesc(CN), (jo > 0 || f > 0) ? 1u : 0u);
-                    }
-                    issued = true;
-                    ptx::mma_commit_elect(bar(C::WE + s));
-                }
-                if (!ok) break;
-                ptx::mma_commit_elect(bar(C::HE + hb));
-                if (jo == p.chunks - 1) {
-                    ptx::mma_commit_elect(bar(C::OF));
-                    ++t;
-                }
-            }
+            if (!ok) break;
+            ptx::mma_commit_elect(bar(C::GF));
             if (++j == p.chunks) {
                 j = 0;
-                xfirst += p.kc;
+                xn += p.kc;
             }
         }
         if (!ok && issued) {
@@ -702,30 +692,92 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
             wait_bounded(bar(C::DRAIN), 0, nullptr);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // --------------------------------------------------------- OUT products
+        int j = 0, t = 0;  // chunk of the tile, tile
+        bool ok = true, issued = false;
+        for (int q = 0; q < total && ok; ++q) {
+            // Y += H(q) Wd^T
+            if (j == 0) {  // the tile before has been drained
+                ok = wait_warp(bar(C::OE), (t & 1) ^ 1, abort_flag);
+                if (!ok) break;
+            }
+            ok = wait_warp(bar(C::HF), uint32_t(q) & 1u, abort_flag);
+            if (!ok) break;
+            ok = wait_warp(bar(C::GC), uint32_t(min(q + 1, total - 1)) & 1u, abort_flag);  // GU(q + 1)
+            if (!ok) break;
+            const int n0 = min(q + 2, total) * p.kc + q * C::OUT_STAGES;
+            for (int k = 0; k < C::OUT_STAGES; ++k) {
+                const int n = n0 + k, s = n % C::STAGES;
+                ok = weights_full(n);
+                if (!ok) break;
+                if (k == C::OUT_STAGES - 1) ptx::mbar_arrive_elect(bar(C::OC));
+                ptx::tc_fence_after();
+                const uint32_t h = sb + uint32_t(C::OFF_H), b = sb + uint32_t(C::OFF_W + 32768 * s);
+#pragma unroll
+                for (int kk = 0; kk < 8 / C::OUT_STAGES; ++kk) {
+                    const int f = kk + 4 * k;  // 16-feature step of the chunk
+                    ptx::mma_ss_elect(tmem + 256u, desc_k_major<128>(h + 16384 * (f >> 2) + 32 * (f & 3)),
+                                      desc_k_major<128>(b + (CN == 128 ? 16384 * (f >> 2) : 0) + 32 * (f & 3)),
+                                      C::idesc(CN), (j > 0 || f > 0) ? 1u : 0u);
+                }
+                issued = true;
+                ptx::mma_commit_elect(bar(C::WE + s));
+            }
+            if (!ok) break;
+            ptx::mma_commit_elect(bar(C::HE));
+            if (++j == p.chunks) {
+                ptx::mma_commit_elect(bar(C::OF));
+                j = 0;
+                ++t;
+            }
+        }
+        if (!ok && issued) {
+            ptx::mma_commit_elect(bar(C::DRAIN + 1));
+            wait_bounded(bar(C::DRAIN + 1), 0, nullptr);
+        }
+        __syncwarp();
     } else if (warp >= 4) {
         // ----------------------------------------------------------- epilogue
-        const int wq = warp & 3, half = (warp - 4) >> 2;
+        const int wq = warp & 3, quarter = (warp - 4) >> 2;
         const int r = 32 * wq + lane;
         const uint32_t tl = tmem + (uint32_t(32 * wq) << 16);
         bool ok = true;
         int tile = blockIdx.x, j = 0, t = 0;
+        const uint32_t ys = sb + uint32_t(C::OFF_Y + 2048 * (warp - 4));
+        // 32 channels at a time of this warp's rows of Y; the tile of the call before has left `ys`
         auto drain = [&](int of_tile) -> bool {
             if (!wait_warp(bar(C::OF), uint32_t(t) & 1u, abort_flag)) return false;
             ptx::tc_fence_after();
             const int m = 128 * of_tile + r;
-            uint16_t* row = p.out + size_t(m) * p.C;
 #pragma unroll 1
-            for (int c = 0; c < CN / 64; ++c) {
+            for (int c = 0; c < CN / 128; ++c) {
                 float v[32];
-                const int c0 = CN / 2 * half + 32 * c;
+                const int c0 = CN / 4 * quarter + 32 * c;
                 ptx::tmem_ld_x32(tl + uint32_t(256 + c0), reinterpret_cast<uint32_t*>(v));
                 ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
-                if (c == CN / 64 - 1) {
+                if (c == CN / 128 - 1) {
                     ptx::tc_fence_before();
                     ptx::mbar_arrive_elect(bar(C::OE));
                 }
-                if (m < p.M) tr_store_row<F16>(row, c0, p.C, p.wide_store, v);
-                __syncwarp();
+                if (p.wide_store) {
+                    ptx::bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        ptx::st_shared_v4(ys + swz_chunk<64>(lane, e),
+                                          make_uint4(tr_pack<F16>(v[8 * e], v[8 * e + 1]), tr_pack<F16>(v[8 * e + 2], v[8 * e + 3]),
+                                                     tr_pack<F16>(v[8 * e + 4], v[8 * e + 5]),
+                                                     tr_pack<F16>(v[8 * e + 6], v[8 * e + 7])));
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    const int m0 = 128 * of_tile + 32 * wq;
+                    if (lane == 0 && m0 < p.M && c0 < p.C) ptx::tma_store_2d(&maps.m[4], ys, c0, m0);
+                    __syncwarp();
+                } else {
+                    if (m < p.M) tr_store_row<F16>(p.out + size_t(m) * p.C, c0, p.C, 0, v);
+                    __syncwarp();
+                }
             }
             ++t;
             return true;
@@ -734,38 +786,30 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
             ok = wait_warp(bar(C::GF), uint32_t(q) & 1u, abort_flag);
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t h = sb + uint32_t(C::OFF_H + 32768 * (q & 1) + 16384 * half);
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                float g[32], u[32];
-                ptx::tmem_ld_x32(tl + uint32_t(64 * half + 32 * c), reinterpret_cast<uint32_t*>(g));
-                ptx::tmem_ld_x32(tl + uint32_t(128 + 64 * half + 32 * c), reinterpret_cast<uint32_t*>(u));
-                ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
-                ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
-                if (c == 1) {
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive_elect(bar(C::GE));
-                }
-                if (c == 0) {  // the product that read this H tile last is done
-                    ok = wait_warp(bar(C::HE + (q & 1)), uint32_t((q >> 1) & 1) ^ 1u, abort_flag);
-                    if (!ok) break;
-                }
+            float g[32], u[32];
+            ptx::tmem_ld_x32(tl + uint32_t(32 * quarter), reinterpret_cast<uint32_t*>(g));
+            ptx::tmem_ld_x32(tl + uint32_t(128 + 32 * quarter), reinterpret_cast<uint32_t*>(u));
+            ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
+            ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
+            ptx::tc_fence_before();
+            ptx::mbar_arrive_elect(bar(C::GE));
+            uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int o = 8 * e + 2 * i;
-                        const float2 hv = tr_gate2<ACT>(make_float2(g[o], g[o + 1]), make_float2(u[o], u[o + 1]));
-                        w[i] = tr_pack<F16>(hv.x, hv.y);
-                    }
-                    ptx::st_shared_v4(h + swz_chunk<128>(r, 4 * c + e), make_uint4(w[0], w[1], w[2], w[3]));
-                }
+            for (int e = 0; e < 16; ++e) {
+                const float2 hv = tr_gate2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]));
+                w[e] = tr_pack<F16>(hv.x, hv.y);
             }
+            // the product of the chunk before has read the H tile
+            ok = wait_warp(bar(C::HE), uint32_t(q & 1) ^ 1u, abort_flag);
             if (!ok) break;
+            const uint32_t h = sb + uint32_t(C::OFF_H + 16384 * (quarter >> 1));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ptx::st_shared_v4(h + swz_chunk<128>(r, 4 * (quarter & 1) + e),
+                                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
             ptx::fence_proxy_async_smem();  // H is read by the tensor cores
             __syncwarp();
-            ptx::mbar_arrive_elect(bar(C::HF + (q & 1)));
+            ptx::mbar_arrive_elect(bar(C::HF));
             if (j == 0 && q > 0) ok = drain(tile - G);
             if (++j == p.chunks) {
                 j = 0;
@@ -773,6 +817,8 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
             }
         }
         if (ok && total > 0) drain(tile - G);
+        ptx::bulk_wait_all();  // the stores have left shared memory and are done
+        __syncwarp();
     }
 
     ptx::tc_fence_before();
