@@ -490,8 +490,11 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
 // weights stream through a ring (from L2, where they stay), H never leaves the
 // SM.  Per chunk of 128 features: G and U (one N = 256 MMA a step) into 256
 // columns of tensor memory; the epilogue warps turn them into a 128 x 128 tile
-// of H in shared memory (swizzled as the tensor core reads it); Y += H Wd^T
-// accumulates in CN columns of tensor memory.  One warp issues the products GU,
+// of H; Y += H Wd^T accumulates in CN columns of tensor memory.  At CN = 128 H
+// lies in tensor memory too, as the A operand of its product: the MMAs' operand
+// reads and the weights' arrival already take most of the 128 bytes a cycle of
+// shared memory, and H there would add a write and a read.  At CN = 256 tensor
+// memory is full and H goes to shared memory, swizzled as the tensor core reads it.  One warp issues the products GU,
 // another OUT (an issuing warp is busy for most of an MMA's time, so one would
 // leave the tensor cores idle at its waits); GU(q + 1) runs beside the activation
 // of chunk q, across tiles too, and a tile's Y is drained after the first
@@ -514,10 +517,11 @@ struct TrFusedCfg {
     static constexpr int EPI_WARPS = 16;           // a warp: 32 rows x 32 features of a chunk
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int XSLOTS = 4;               // 128 rows x 64 k of X, 16 KB each
-    static constexpr int STAGES = 3;               // weights: 32 KB each
+    static constexpr bool H_TMEM = CN == 128;
+    static constexpr int STAGES = H_TMEM ? 4 : 3;  // weights: 32 KB each
     static constexpr int OUT_STAGES = CN / 128;    // ring stages of Wd for a chunk
     static constexpr int OFF_H = XSLOTS * 16384;   // 128 rows x 128 features
-    static constexpr int OFF_Y = OFF_H + 32768;    // 2 KB a warp: 32 rows x 32 channels of Y
+    static constexpr int OFF_Y = OFF_H + (H_TMEM ? 0 : 32768);    // 2 KB a warp: 32 rows x 32 channels of Y
     static constexpr int OFF_W = OFF_Y + EPI_WARPS * 2048;
     static constexpr int OFF_BAR = OFF_W + STAGES * 32768;
     static constexpr int XF = 0, XE = XF + XSLOTS, WF = XE + XSLOTS, WE = WF + STAGES, GF = WE + STAGES, GE = GF + 1,
@@ -526,7 +530,7 @@ struct TrFusedCfg {
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-    static constexpr uint32_t TMEM_COLS = 512;     // G, U: 0-255, Y: 256 - 256 + CN - 1
+    static constexpr uint32_t TMEM_COLS = 512;     // G, U: 0-255, Y: CN columns from 256, H: 64 columns from 384
     static constexpr uint32_t AB = F16 ? 0u : ((1u << 7) | (1u << 10));
     __host__ __device__ static constexpr uint32_t idesc(int n) {
         return (1u << 4) | AB | ((uint32_t(n) >> 3) << 17) | ((128u >> 4) << 24);
@@ -713,13 +717,17 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
                 if (!ok) break;
                 if (k == C::OUT_STAGES - 1) ptx::mbar_arrive_elect(bar(C::OC));
                 ptx::tc_fence_after();
-                const uint32_t h = sb + uint32_t(C::OFF_H), b = sb + uint32_t(C::OFF_W + 32768 * s);
+                const uint32_t b = sb + uint32_t(C::OFF_W + 32768 * s);
 #pragma unroll
                 for (int kk = 0; kk < 8 / C::OUT_STAGES; ++kk) {
                     const int f = kk + 4 * k;  // 16-feature step of the chunk
-                    ptx::mma_ss_elect(tmem + 256u, desc_k_major<128>(h + 16384 * (f >> 2) + 32 * (f & 3)),
-                                      desc_k_major<128>(b + (CN == 128 ? 16384 * (f >> 2) : 0) + 32 * (f & 3)),
-                                      C::idesc(CN), (j > 0 || f > 0) ? 1u : 0u);
+                    const uint64_t db = desc_k_major<128>(b + (CN == 128 ? 16384 * (f >> 2) : 0) + 32 * (f & 3));
+                    const uint32_t add = (j > 0 || f > 0) ? 1u : 0u;
+                    if constexpr (C::H_TMEM)
+                        ptx::mma_ts_elect(tmem + 256u, tmem + uint32_t(384 + 8 * f), db, C::idesc(CN), add);
+                    else
+                        ptx::mma_ss_elect(tmem + 256u, desc_k_major<128>(sb + uint32_t(C::OFF_H + 16384 * (f >> 2) + 32 * (f & 3))),
+                                          db, C::idesc(CN), add);
                 }
                 issued = true;
                 ptx::mma_commit_elect(bar(C::WE + s));
@@ -802,13 +810,20 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
             // the product of the chunk before has read the H tile
             ok = wait_warp(bar(C::HE), uint32_t(q & 1) ^ 1u, abort_flag);
             if (!ok) break;
-            const uint32_t h = sb + uint32_t(C::OFF_H + 16384 * (quarter >> 1));
+            ptx::tc_fence_after();
+            if constexpr (C::H_TMEM) {
+                ptx::tmem_st_x16(tl + uint32_t(384 + 16 * quarter), w);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+            } else {
+                const uint32_t h = sb + uint32_t(C::OFF_H + 16384 * (quarter >> 1));
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                ptx::st_shared_v4(h + swz_chunk<128>(r, 4 * (quarter & 1) + e),
-                                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
-            ptx::fence_proxy_async_smem();  // H is read by the tensor cores
-            __syncwarp();
+                for (int e = 0; e < 4; ++e)
+                    ptx::st_shared_v4(h + swz_chunk<128>(r, 4 * (quarter & 1) + e),
+                                      make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
+                ptx::fence_proxy_async_smem();  // H is read by the tensor cores
+                __syncwarp();
+            }
             ptx::mbar_arrive_elect(bar(C::HF));
             if (j == 0 && q > 0) ok = drain(tile - G);
             if (++j == p.chunks) {
