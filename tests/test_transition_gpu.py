@@ -70,7 +70,8 @@ def test_more_rows_than_one_chunk():
 
 @pytest.mark.parametrize("shape,dt", [((8321, 128, 512), BF16), ((8200, 40, 72), FP16), ((19100, 256, 304), BF16),
                                       ((20001, 192, 136), FP16), ((8193, 100, 130), BF16), ((38000, 64, 128), BF16),
-                                      ((9000, 250, 400), FP16), ((8193, 1, 1), BF16)], ids=str)
+                                      ((9000, 250, 400), FP16), ((8193, 1, 1), BF16), ((60000, 64, 64), BF16),
+                                      ((60001, 128, 40), FP16), ((60000, 96, 192), BF16), ((40000, 136, 100), BF16)], ids=str)
 def test_many_rows_of_few_channels(shape, dt):
     """Sizes at which Y of a row tile is formed without the [M, F] array: one and
     several tiles a CTA, one and several feature chunks, C up to 128 and up to 256."""
