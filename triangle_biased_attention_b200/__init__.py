@@ -19,7 +19,6 @@ fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -450,6 +449,8 @@ def trimul(a: torch.Tensor, b: torch.Tensor, outgoing: bool = True, out: Optiona
 
 
 def _same(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
@@ -460,16 +461,27 @@ def _same(name: str, t: torch.Tensor, shape, dtype, device) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _call_stream(stream: Optional[torch.cuda.Stream], device):
-    """The stream of a call and a context in which its outputs and workspace are
-    allocated, so that they belong to that stream."""
-    if device.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device")
-    if stream is None:
-        return torch.cuda.current_stream(device), contextlib.nullcontext()
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return stream, torch.cuda.stream(stream)
+class _OnStream:
+    """The stream of a call.  Inside the context the call's outputs and workspace
+    are allocated, so that they belong to that stream."""
+
+    __slots__ = ("handle", "scope")
+
+    def __init__(self, stream: Optional[torch.cuda.Stream], device):
+        if device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self.scope = None if stream is None else torch.cuda.stream(stream)
+        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        if self.scope is not None:
+            self.scope.__enter__()
+
+    def __exit__(self, *exc):
+        if self.scope is not None:
+            self.scope.__exit__(*exc)
 
 
 def _workspace(workspace: Optional[torch.Tensor], need: int, device, what: str) -> torch.Tensor:
@@ -517,9 +529,9 @@ def transition(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down
     ``stream`` (default: the current stream) without synchronising.
     """
     M, C, F = _transition_args(x, w_gate, w_up, w_down, act)
-    stream, scope = _call_stream(stream, x.device)
+    on = _OnStream(stream, x.device)
     code = _DTYPES[x.dtype]
-    with scope:
+    with on:
         if out is None:
             out = torch.empty_like(x)
         else:
@@ -528,7 +540,7 @@ def transition(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down
                                "evo_transition_fwd_workspace_size")
     status = evo_transition_fwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), out.data_ptr(),
                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), M, C, F, _ACTS[act],
-                                code, stream.cuda_stream)
+                                code, on.handle)
     if status != EVO_OK:
         raise EvoAttnError(status, "evo_transition_fwd")
     return out
@@ -548,9 +560,9 @@ def transition_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tenso
     """
     M, C, F = _transition_args(x, w_gate, w_up, w_down, act)
     _same("dy", dy, x.shape, x.dtype, x.device)
-    stream, scope = _call_stream(stream, x.device)
+    on = _OnStream(stream, x.device)
     code = _DTYPES[x.dtype]
-    with scope:
+    with on:
         dx = torch.empty_like(x) if need_dx else None
         dw = [torch.empty_like(w) for w in (w_gate, w_up, w_down)] if need_dw else [None] * 3
         workspace = _workspace(workspace, evo_transition_bwd_workspace_size(M, C, F, code), x.device,
@@ -558,7 +570,7 @@ def transition_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tenso
     status = evo_transition_bwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), dy.data_ptr(),
                                 _ptr(dx), _ptr(dw[0]), _ptr(dw[1]), _ptr(dw[2]), workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), M, C, F, _ACTS[act], code,
-                                stream.cuda_stream)
+                                on.handle)
     if status != EVO_OK:
         raise EvoAttnError(status, "evo_transition_bwd")
     return dx, dw[0], dw[1], dw[2]
@@ -640,15 +652,15 @@ def relpos_bias(table: torch.Tensor, borders: torch.Tensor, pos: torch.Tensor, p
     shape = (B, 1, H, Sq, Sk)
     if base is not None:
         _same("base", base, shape, table.dtype, table.device)
-    stream, scope = _call_stream(stream, table.device)
+    on = _OnStream(stream, table.device)
     if out is None:
-        with scope:
-            out = torch.empty(shape, dtype=table.dtype, device=table.device)
+        with on:
+            out = table.new_empty(shape)
     else:
         _same("out", out, shape, table.dtype, table.device)
     status = evo_relpos_fwd(table.data_ptr(), borders.data_ptr(), pos.data_ptr(), pos_k.data_ptr(), _ptr(chain),
                             _ptr(chain_k), _ptr(base), out.data_ptr(), B, Sq, Sk, H, nb, _DTYPES[table.dtype],
-                            stream.cuda_stream)
+                            on.handle)
     if status != EVO_OK:
         raise EvoAttnError(status, "evo_relpos_fwd")
     return out
@@ -670,16 +682,16 @@ def relpos_bias_backward(dpair: torch.Tensor, borders: torch.Tensor, pos: torch.
     pos_k, chain_k, B, Sq, Sk, nb = _relpos_args(borders, pos, pos_k, chain, chain_k, dpair.device)
     H = dpair.shape[2]
     _same("dpair", dpair, (B, 1, H, Sq, Sk), dpair.dtype, dpair.device)
-    stream, scope = _call_stream(stream, dpair.device)
+    on = _OnStream(stream, dpair.device)
     has_chain = chain is not None
-    with scope:
+    with on:
         dtable = torch.empty((nb + 1 + has_chain, H), dtype=dpair.dtype, device=dpair.device)
         workspace = _workspace(workspace, evo_relpos_bwd_workspace_size(B, Sq, Sk, H, nb, int(has_chain)), dpair.device,
                                "evo_relpos_bwd_workspace_size")
     status = evo_relpos_bwd(dpair.data_ptr(), borders.data_ptr(), pos.data_ptr(), pos_k.data_ptr(), _ptr(chain),
                             _ptr(chain_k), dtable.data_ptr(), workspace.data_ptr(),
                             workspace.numel() * workspace.element_size(), B, Sq, Sk, H, nb, _DTYPES[dpair.dtype],
-                            stream.cuda_stream)
+                            on.handle)
     if status != EVO_OK:
         raise EvoAttnError(status, "evo_relpos_bwd")
     return dtable

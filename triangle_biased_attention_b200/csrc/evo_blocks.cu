@@ -604,9 +604,9 @@ int check_relpos(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t nb, int d
 }
 
 // Threads of a block along j, as a power of two: no more than the key columns need.
-int rel_lane_cols(int64_t Sk, int most) {
+int rel_lane_cols(int64_t Sk, int cols, int most) {
     int l = 0;
-    while (l < most && (int64_t(evo::kRelCols) << l) < Sk) ++l;
+    while (l < most && (int64_t(cols) << l) < Sk) ++l;
     return l;
 }
 
@@ -620,13 +620,14 @@ struct RelTiles {
 // clearing and adding up the block's bins, low enough that the blocks fill the SMs.
 RelTiles rel_bwd_tiles(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t rows) {
     RelTiles t;
-    t.lane_cols = rel_lane_cols(Sk, 7);
-    t.jt = (Sk + (int64_t(evo::kRelCols) << t.lane_cols) - 1) / (int64_t(evo::kRelCols) << t.lane_cols);
+    t.lane_cols = rel_lane_cols(Sk, evo::kRelBwdCols, 7);
+    const int64_t width = int64_t(evo::kRelBwdCols) << t.lane_cols;
+    t.jt = (Sk + width - 1) / width;
     t.chunks = (rows + evo::kRelBins - 1) / evo::kRelBins;
     const int64_t per = evo::kRelBwdThreads >> t.lane_cols;  // query rows at once
     const int64_t others = std::max<int64_t>(1, B * H * t.jt);
     const int64_t want = std::max<int64_t>(1, 148 * 6 / others);
-    int64_t ti = std::max<int64_t>((Sq + want - 1) / want, 16 * per);
+    int64_t ti = std::max<int64_t>((Sq + want - 1) / want, 8 * per);
     ti = std::max<int64_t>(ti, (Sq + 65534) / 65535);
     t.ti = int(std::min<int64_t>((ti + per - 1) / per * per, kIntMax / 4));
     t.it = (Sq + t.ti - 1) / t.ti;
@@ -634,19 +635,38 @@ RelTiles rel_bwd_tiles(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t row
     return t;
 }
 
+template <typename T, int NW, bool VEC>
+int launch_relpos_fwd(int dev, evo::RelParams<T> p, cudaStream_t st) {
+    constexpr int heads = NW * 4 / int(sizeof(T)), cols = VEC ? 16 / int(sizeof(T)) : evo::kRelCols;
+    p.groups = (p.H + heads - 1) / heads;
+    p.lane_cols = rel_lane_cols(p.Sk, cols, 8);
+    const int64_t width = int64_t(cols) << p.lane_cols, jt = (p.Sk + width - 1) / width;
+    const int64_t per = evo::kRelThreads >> p.lane_cols;
+    // about six blocks a SM: each fills its tables once for all its rows
+    const int64_t others = jt * p.B * p.groups;
+    int64_t ti = (p.Sq * others + 148 * 6 - 1) / (148 * 6);
+    ti = std::max<int64_t>(ti, (int64_t(p.Sq) + 65534) / 65535);
+    p.ti = int((ti + per - 1) / per * per);
+    if (int64_t(p.B) * p.groups > 65535) return EVO_ERR_UNSUPPORTED_SHAPE;
+    const int smem = evo::rel_smem((p.rows * NW * 4 + 15) / 16 * 16, p.nb);
+    auto kernel = evo::evo_relpos_fwd_kernel<T, NW, VEC>;
+    static AttrOnce attr;
+    if (!attr.ensure(dev, kernel, evo::rel_smem((evo::kRelMaxBorders + 4) * NW * 4, evo::kRelMaxBorders))) return EVO_ERR_CUDA;
+    const dim3 grid{unsigned(jt), blocks_of(p.Sq, p.ti), unsigned(p.B * p.groups)};
+    return launch(kernel, grid, evo::kRelThreads, smem, st, p) ? EVO_OK : EVO_ERR_CUDA;
+}
+
 template <typename T>
-int run_relpos_fwd(evo::RelParams<T> p, const void* table, const void* base, void* pair, cudaStream_t st) {
+int run_relpos_fwd(int dev, evo::RelParams<T> p, const void* table, const void* base, void* pair, cudaStream_t st) {
     p.table = static_cast<const T*>(table);
     p.base = static_cast<const T*>(base);
     p.pair = static_cast<T*>(pair);
-    p.lane_cols = rel_lane_cols(p.Sk, 8);
-    const int64_t cols = int64_t(evo::kRelCols) << p.lane_cols;
-    const int64_t jt = (p.Sk + cols - 1) / cols;
-    const int per = evo::kRelThreads >> p.lane_cols;
-    int64_t ti = std::max<int64_t>(4 * per, (int64_t(p.Sq) + 65534) / 65535);
-    p.ti = int((ti + per - 1) / per * per);
-    const dim3 grid{unsigned(jt), blocks_of(p.Sq, p.ti), unsigned(p.B)};
-    return launch(evo::evo_relpos_fwd_kernel<T>, grid, evo::kRelThreads, 0, st, p) ? EVO_OK : EVO_ERR_CUDA;
+    const bool vec = p.Sk % (16 / int(sizeof(T))) == 0 && aligned(pair, 16) && (!base || aligned(base, 16));
+    // as many heads in a 16-, 8- or 4-byte table row as there are
+    const int words = int((p.H * int64_t(sizeof(T)) + 3) / 4);
+    if (words > 2) return vec ? launch_relpos_fwd<T, 4, true>(dev, p, st) : launch_relpos_fwd<T, 4, false>(dev, p, st);
+    if (words > 1) return vec ? launch_relpos_fwd<T, 2, true>(dev, p, st) : launch_relpos_fwd<T, 2, false>(dev, p, st);
+    return vec ? launch_relpos_fwd<T, 1, true>(dev, p, st) : launch_relpos_fwd<T, 1, false>(dev, p, st);
 }
 
 template <typename T>
@@ -656,10 +676,14 @@ int run_relpos_bwd(int dev, evo::RelParams<T> p, const void* dpair, void* dtable
     p.part = static_cast<float*>(ws);
     p.lane_cols = t.lane_cols;
     p.ti = t.ti;
-    auto kernel = evo::evo_relpos_bwd_kernel<T>;
-    static AttrOnce attr;
-    if (!attr.ensure(dev, kernel, evo::kRelBins * evo::kRelBwdThreads * 4)) return EVO_ERR_CUDA;
-    const int smem = std::min(p.rows, evo::kRelBins) * evo::kRelBwdThreads * 4;
+    const bool vec = p.Sk % (16 / int(sizeof(T))) == 0 && aligned(dpair, 16);
+    const bool chains = p.chain_q != nullptr;
+    auto kernel = vec ? (chains ? evo::evo_relpos_bwd_kernel<T, true, true> : evo::evo_relpos_bwd_kernel<T, true, false>)
+                      : (chains ? evo::evo_relpos_bwd_kernel<T, false, true> : evo::evo_relpos_bwd_kernel<T, false, false>);
+    static AttrOnce attrs[4];
+    if (!attrs[2 * vec + chains].ensure(dev, kernel, evo::rel_smem(evo::kRelBins * evo::kRelBwdThreads * 4, evo::kRelMaxBorders)))
+        return EVO_ERR_CUDA;
+    const int smem = evo::rel_smem(std::min(p.rows, evo::kRelBins) * evo::kRelBwdThreads * 4, p.nb);
     const dim3 grid{unsigned(t.jt), unsigned(t.it), unsigned(p.B * p.H * t.chunks)};
     if (!launch(kernel, grid, evo::kRelBwdThreads, smem, st, p)) return EVO_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -717,7 +741,7 @@ extern "C" EVO_API int evo_relpos_fwd(const void* table, const int32_t* borders,
     if (dev < 0) return dev;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 #define EVO_REL_FWD(T) \
-    return run_relpos_fwd<T>(rel_params<T>(borders, pos_q, pos_k, chain_q, chain_k, B, Sq, Sk, H, num_borders), table, base, pair, st)
+    return run_relpos_fwd<T>(dev, rel_params<T>(borders, pos_q, pos_k, chain_q, chain_k, B, Sq, Sk, H, num_borders), table, base, pair, st)
     if (dtype == EVO_DTYPE_FP32) EVO_REL_FWD(float);
     if (dtype == EVO_DTYPE_FP16) EVO_REL_FWD(__half);
     EVO_REL_FWD(__nv_bfloat16);

@@ -6,24 +6,28 @@
 //     r(b, i, j)        = the number of borders <= pos_q[b, i] - pos_k[b, j],
 //                         or num_borders + 1 where the chains of i and j differ
 //
-// A thread owns eight key columns j and walks the query rows i, so the key
+// A thread owns a few key columns j and walks the query rows i, so the key
 // positions stay in registers.  A distance finds its row in one shared-memory
-// read when the borders span at most kRelLut - 2 distances (every distance between the
-// first and the last border has an entry), else by a binary search in the
-// borders.
+// read when the borders span at most kRelLut - 2 distances (every distance
+// between the first and the last border has an entry), else by a binary search
+// in the borders.  Both kernels are bound by memory: the forward by writing P
+// (and reading the base), the backward by reading dP once.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace evo {
 
 constexpr int kRelThreads = 256;      // forward
+constexpr int kRelCols = 8;           // key columns of a forward thread
 constexpr int kRelBwdThreads = 128;   // backward
-constexpr int kRelCols = 8;           // key columns of a thread
+constexpr int kRelBwdCols = 8;        // key columns of a backward thread
 constexpr int kRelLut = 2048;         // entries of the distance table
 constexpr int kRelMaxBorders = 2048;
 constexpr int kRelBins = 256;         // table rows that one backward block sums
@@ -39,6 +43,7 @@ struct RelParams {
     int B, Sq, Sk, H, nb, rows;
     int ti;               // query rows of a block
     int lane_cols;        // log2 of the threads along j
+    int groups;           // forward: groups of heads
 };
 
 // difference of two positions, held at the ends of the 32-bit range
@@ -107,34 +112,112 @@ __device__ __forceinline__ T rel_from(float v) {
     else return __float2bfloat16_rn(v);
 }
 
-// One block: `ti` query rows x 256 or more key columns x every head.
+// Shared memory of a block, in this order: the table rows or the sums, the
+// borders, the distance table.
+__host__ __device__ inline int rel_smem(int head_bytes, int nb) { return head_bytes + (nb + 3) / 4 * 16 + kRelLut * 2; }
+
+// The pair (a, b) of 16-bit values at half `hi` of two words, as one word.
+__device__ __forceinline__ uint32_t rel_halves(uint32_t a, uint32_t b, int hi) {
+    return __byte_perm(a, b, hi ? 0x7632 : 0x5410);
+}
+
+// sum of two packed pairs (or two floats) in fp32, rounded to the type
 template <typename T>
-__global__ void __launch_bounds__(kRelThreads) evo_relpos_fwd_kernel(const RelParams<T> p) {
-    __shared__ int sborders[kRelMaxBorders];
-    __shared__ uint16_t lut[kRelLut];
+__device__ __forceinline__ uint32_t rel_add(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    } else if constexpr (std::is_same<T, __half>::value) {
+        const float2 x = __half22float2(reinterpret_cast<const __half2&>(a));
+        const float2 y = __half22float2(reinterpret_cast<const __half2&>(b));
+        return ptx::pack_f16x2(x.x + y.x, x.y + y.y);
+    } else {
+        return ptx::pack_bf16x2(ptx::bf16lo_to_f32(a) + ptx::bf16lo_to_f32(b), ptx::bf16hi_to_f32(a) + ptx::bf16hi_to_f32(b));
+    }
+}
+
+// One block: `ti` query rows x the key columns of its threads x a group of heads.
+// The group's part of the table lies in shared memory, NW words a row (NW * 4 /
+// sizeof(T) heads), so one read fetches a pair's value for every head of the
+// group.  VEC: a thread's columns are 16 whole bytes of each head's row of P,
+// written at once (the values of its columns are transposed in registers); else
+// its columns lie the block's width apart and are written one by one.
+template <typename T, int NW, bool VEC>
+__global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const RelParams<T> p) {
+    constexpr int HEADS = NW * 4 / int(sizeof(T));
+    constexpr int COLS = VEC ? 16 / int(sizeof(T)) : kRelCols;
+    extern __shared__ __align__(16) uint8_t rel_sm[];
+    T* stable = reinterpret_cast<T*>(rel_sm);
+    int* sborders = reinterpret_cast<int*>(rel_sm + (p.rows * NW * 4 + 15) / 16 * 16);
+    uint16_t* lut = reinterpret_cast<uint16_t*>(sborders + (p.nb + 3) / 4 * 4);
+    const int b = blockIdx.z / p.groups, h0 = (blockIdx.z % p.groups) * HEADS, nh = min(HEADS, p.H - h0);
+    for (int i = threadIdx.x; i < p.rows * HEADS; i += kRelThreads) {
+        const int r = i / HEADS, h = i % HEADS;
+        stable[i] = h < nh ? p.table[(long long)r * p.H + h0 + h] : rel_from<T>(0.0f);
+    }
     const RelLookup L = rel_setup(p.borders, p.nb, sborders, lut);
     const int lanes = 1 << p.lane_cols, tx = threadIdx.x & (lanes - 1), ty = threadIdx.x >> p.lane_cols;
-    const int b = blockIdx.z, j0 = blockIdx.x * lanes * kRelCols + tx;
+    const int j0 = blockIdx.x * lanes * COLS + (VEC ? tx * COLS : tx), step = VEC ? 1 : lanes;
     const int i_end = min(p.Sq, int(blockIdx.y + 1) * p.ti);
-    int pk[kRelCols], ck[kRelCols];
+    int pk[COLS], ck[COLS];
 #pragma unroll
-    for (int e = 0; e < kRelCols; ++e) {
-        const int j = j0 + e * lanes;
+    for (int e = 0; e < COLS; ++e) {
+        const int j = j0 + e * step;
         pk[e] = j < p.Sk ? p.pos_k[(long long)b * p.Sk + j] : 0;
         ck[e] = j < p.Sk && p.chain_k ? p.chain_k[(long long)b * p.Sk + j] : 0;
     }
-    for (int i = blockIdx.y * p.ti + ty; i < i_end; i += blockDim.x >> p.lane_cols) {
+    if (j0 >= p.Sk) return;
+    const long long plane = (long long)p.Sq * p.Sk;
+    for (int i = blockIdx.y * p.ti + ty; i < i_end; i += kRelThreads >> p.lane_cols) {
         const int pq = p.pos_q[(long long)b * p.Sq + i];
         const int cq = p.chain_q ? p.chain_q[(long long)b * p.Sq + i] : 0;
+        const long long at = ((long long)b * p.H + h0) * plane + (long long)i * p.Sk + j0;
+        uint4 base[VEC ? HEADS : 1];
+        if (VEC && p.base) {  // in flight while the rows are looked up
 #pragma unroll
-        for (int e = 0; e < kRelCols; ++e) {
-            const int j = j0 + e * lanes;
-            if (j >= p.Sk) continue;
+            for (int h = 0; h < HEADS; ++h)
+                if (h < nh) base[h] = *reinterpret_cast<const uint4*>(p.base + at + h * plane);
+        }
+        uint32_t v[COLS][NW];  // a column's values, HEADS of them
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) {
             const int r = cq == ck[e] ? L.row(rel_distance(pq, pk[e])) : p.nb + 1;
-            for (int h = 0; h < p.H; ++h) {
-                const long long at = (((long long)b * p.H + h) * p.Sq + i) * p.Sk + j;
-                const T t = p.table[(long long)r * p.H + h];
-                p.pair[at] = p.base ? rel_from<T>(rel_f32(t) + rel_f32(p.base[at])) : t;
+            if constexpr (NW == 4) {
+                const uint4 w = *reinterpret_cast<const uint4*>(rel_sm + r * 16);
+                v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+            } else if constexpr (NW == 2) {
+                const uint2 w = *reinterpret_cast<const uint2*>(rel_sm + r * 8);
+                v[e][0] = w.x, v[e][1] = w.y;
+            } else {
+                v[e][0] = *reinterpret_cast<const uint32_t*>(rel_sm + r * 4);
+            }
+        }
+        if constexpr (VEC) {
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                if (h >= nh) break;
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = sizeof(T) == 4 ? v[k][h % NW] : rel_halves(v[(2 * k) % COLS][(h / 2) % NW], v[(2 * k + 1) % COLS][(h / 2) % NW], h & 1);
+                if (p.base) {
+                    w[0] = rel_add<T>(w[0], base[h].x);
+                    w[1] = rel_add<T>(w[1], base[h].y);
+                    w[2] = rel_add<T>(w[2], base[h].z);
+                    w[3] = rel_add<T>(w[3], base[h].w);
+                }
+                *reinterpret_cast<uint4*>(p.pair + at + h * plane) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) {
+                if (j0 + e * step >= p.Sk) break;
+#pragma unroll
+                for (int h = 0; h < HEADS; ++h) {
+                    if (h >= nh) break;
+                    const T t = reinterpret_cast<const T*>(v[e])[h];
+                    const long long o = at + h * plane + (long long)e * step;
+                    p.pair[o] = p.base ? rel_from<T>(rel_f32(t) + rel_f32(p.base[o])) : t;
+                }
             }
         }
     }
@@ -143,61 +226,113 @@ __global__ void __launch_bounds__(kRelThreads) evo_relpos_fwd_kernel(const RelPa
 // One block: `ti` query rows x 128 threads' key columns of one head, table rows
 // [bin0, bin0 + kRelBins).  Each thread sums into its own column of shared
 // memory, [bin][thread], so no two threads meet and the order of the additions
-// is fixed; while a key column stays in one bucket its sum stays in a register.
-template <typename T>
-__global__ void __launch_bounds__(kRelBwdThreads) evo_relpos_bwd_kernel(const RelParams<T> p) {
-    extern __shared__ float bins[];  // [min(rows - bin0, kRelBins)][128]
-    __shared__ int sborders[kRelMaxBorders];
-    __shared__ uint16_t lut[kRelLut];
+// is fixed.  While no column of a warp leaves its bucket the sums stay in
+// registers; when one does, the warp adds all of them to their bins, without a
+// branch for each (branches for each column, or taking only the columns that
+// moved, cost 5 times as much: near the diagonal most rows move some column).
+// The next row's values are in flight meanwhile.  VEC: a thread's columns are
+// runs of 16 whole bytes; else they lie the block's width apart.
+template <typename T, bool VEC, bool CHAINS>
+__global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const RelParams<T> p) {
+    constexpr int RUN = VEC ? 16 / int(sizeof(T)) : 1;  // adjacent columns
+    constexpr int COLS = kRelBwdCols;
+    extern __shared__ __align__(16) uint8_t rel_sm[];
     const int jt = blockIdx.x, itile = blockIdx.y;
     const int chunks = (p.rows + kRelBins - 1) / kRelBins;
     const int bin0 = (blockIdx.z % chunks) * kRelBins, nbins = min(kRelBins, p.rows - bin0);
     const int bh = blockIdx.z / chunks, b = bh / p.H, h = bh % p.H;
-    for (int i = threadIdx.x; i < nbins * kRelBwdThreads; i += kRelBwdThreads) bins[i] = 0.0f;
-    const RelLookup L = rel_setup(p.borders, p.nb, sborders, lut);
+    float* bins = reinterpret_cast<float*>(rel_sm);  // [nbins][128]
+    int* sborders = reinterpret_cast<int*>(bins + min(p.rows, kRelBins) * kRelBwdThreads);
+    uint16_t* lut = reinterpret_cast<uint16_t*>(sborders + (p.nb + 3) / 4 * 4);
+    for (int i = threadIdx.x; i < nbins * (kRelBwdThreads / 4); i += kRelBwdThreads)
+        reinterpret_cast<float4*>(bins)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int lanes = 1 << p.lane_cols, tx = threadIdx.x & (lanes - 1), ty = threadIdx.x >> p.lane_cols;
-    const int j0 = jt * lanes * kRelCols + tx, i_end = min(p.Sq, (itile + 1) * p.ti);
-    int pk[kRelCols], ck[kRelCols], cur[kRelCols];
-    float sum[kRelCols];
+    const int j0 = jt * lanes * COLS + tx * RUN, i_end = min(p.Sq, (itile + 1) * p.ti), di = kRelBwdThreads >> p.lane_cols;
+    auto col = [&](int e) -> int { return j0 + (e / RUN) * lanes * RUN + e % RUN; };
+    constexpr int WORDS = VEC ? COLS * int(sizeof(T)) / 4 : COLS;  // a row's values as loaded
+    auto fetch = [&](int i, uint32_t (&w)[WORDS]) {
+        const T* row = p.dpair + ((long long)bh * p.Sq + i) * p.Sk;
+        if constexpr (VEC) {
 #pragma unroll
-    for (int e = 0; e < kRelCols; ++e) {
-        const int j = j0 + e * lanes;
+            for (int k = 0; k < WORDS / 4; ++k) {
+                const int j = col(k * RUN);
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (i < i_end && j < p.Sk) x = *reinterpret_cast<const uint4*>(row + j);
+                w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) {
+                const int j = col(e);
+                w[e] = i < i_end && j < p.Sk ? __float_as_uint(rel_f32(row[j])) : 0u;
+            }
+        }
+    };
+    auto value = [&](const uint32_t (&w)[WORDS], int e) -> float {
+        if constexpr (!VEC || sizeof(T) == 4) return __uint_as_float(w[e]);
+        else if constexpr (std::is_same<T, __half>::value) return __half2float(reinterpret_cast<const __half*>(w)[e]);
+        else return e & 1 ? ptx::bf16hi_to_f32(w[e / 2]) : ptx::bf16lo_to_f32(w[e / 2]);
+    };
+    uint32_t w[WORDS], next[WORDS];
+    int i = itile * p.ti + ty;
+    fetch(i, w);
+    int pk[COLS], ck[COLS], cur[COLS];
+    float sum[COLS];
+#pragma unroll
+    for (int e = 0; e < COLS; ++e) {
+        const int j = col(e);
         pk[e] = j < p.Sk ? p.pos_k[(long long)b * p.Sk + j] : 0;
-        ck[e] = j < p.Sk && p.chain_k ? p.chain_k[(long long)b * p.Sk + j] : 0;
+        ck[e] = CHAINS && j < p.Sk ? p.chain_k[(long long)b * p.Sk + j] : 0;
         cur[e] = -1;
         sum[e] = 0.0f;
     }
+    const RelLookup L = rel_setup(p.borders, p.nb, sborders, lut);
+    float* mine = bins + threadIdx.x;
     auto flush = [&](int r, float s) {
-        if (r >= bin0 && r < bin0 + nbins) bins[(r - bin0) * kRelBwdThreads + threadIdx.x] += s;
+        if (unsigned(r - bin0) < unsigned(nbins)) mine[(r - bin0) * kRelBwdThreads] += s;
     };
-    for (int i = itile * p.ti + ty; i < i_end; i += kRelBwdThreads >> p.lane_cols) {
+    for (; i < i_end; i += di) {
+        fetch(i + di, next);
         const int pq = p.pos_q[(long long)b * p.Sq + i];
-        const int cq = p.chain_q ? p.chain_q[(long long)b * p.Sq + i] : 0;
-        const T* row = p.dpair + ((long long)bh * p.Sq + i) * p.Sk;
-        float v[kRelCols];
+        const int cq = CHAINS ? p.chain_q[(long long)b * p.Sq + i] : 0;
+        int r[COLS];
+        bool moved = false;
+        if (L.direct) {
 #pragma unroll
-        for (int e = 0; e < kRelCols; ++e) v[e] = j0 + e * lanes < p.Sk ? rel_f32(row[j0 + e * lanes]) : 0.0f;
+            for (int e = 0; e < COLS; ++e) r[e] = L.lut[min(max(rel_distance(pq, pk[e]), L.lo), L.last) - L.lo];
+        } else {
 #pragma unroll
-        for (int e = 0; e < kRelCols; ++e) {
-            const int r = cq == ck[e] ? L.row(rel_distance(pq, pk[e])) : p.nb + 1;
-            if (r != cur[e]) {
-                flush(cur[e], sum[e]);
-                cur[e] = r;
-                sum[e] = 0.0f;
-            }
-            sum[e] += v[e];
+            for (int e = 0; e < COLS; ++e) r[e] = L.search(rel_distance(pq, pk[e]));
         }
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) {
+            if (CHAINS && cq != ck[e]) r[e] = p.nb + 1;
+            moved |= r[e] != cur[e];
+        }
+        if (__any_sync(__activemask(), moved)) {
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) {
+                flush(cur[e], sum[e]);
+                cur[e] = r[e];
+                sum[e] = value(w, e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) sum[e] += value(w, e);
+        }
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) w[k] = next[k];
     }
 #pragma unroll
-    for (int e = 0; e < kRelCols; ++e) flush(cur[e], sum[e]);
+    for (int e = 0; e < COLS; ++e) flush(cur[e], sum[e]);
     __syncthreads();
     // the 128 columns of each bin, a warp a bin, in a fixed order
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long tile = ((long long)b * gridDim.y + itile) * gridDim.x + jt;
+#pragma unroll 4
     for (int r = warp; r < nbins; r += kRelBwdThreads / 32) {
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kRelBwdThreads / 32; ++k) s += bins[r * kRelBwdThreads + 32 * k + lane];
+        const float4 x = reinterpret_cast<const float4*>(bins + r * kRelBwdThreads)[lane];
+        float s = (x.x + x.y) + (x.z + x.w);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) p.part[(tile * p.H + h) * p.rows + bin0 + r] = s;
