@@ -625,11 +625,13 @@ RelTiles rel_bwd_tiles(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t row
     t.jt = (Sk + width - 1) / width;
     t.chunks = (rows + evo::kRelBins - 1) / evo::kRelBins;
     const int64_t per = evo::kRelBwdThreads >> t.lane_cols;  // query rows at once
-    const int64_t others = std::max<int64_t>(1, B * H * t.jt);
-    const int64_t want = std::max<int64_t>(1, 148 * 6 / others);
+    const int64_t others = std::max<int64_t>(1, B * H * t.jt * t.chunks);
+    // one wave: a block's shared memory sets how many an SM holds (five by their registers)
+    const int64_t held = std::min<int64_t>(5, (226 << 10) / (1024 + evo::rel_bwd_smem(int(std::min<int64_t>(rows, evo::kRelBins)), int(rows))));
+    const int64_t want = std::max<int64_t>(1, 148 * std::max<int64_t>(1, held) / others);
     int64_t ti = std::max<int64_t>((Sq + want - 1) / want, 8 * per);
     ti = std::max<int64_t>(ti, (Sq + 65534) / 65535);
-    t.ti = int(std::min<int64_t>((ti + per - 1) / per * per, kIntMax / 4));
+    t.ti = int((ti + per - 1) / per * per);
     t.it = (Sq + t.ti - 1) / t.ti;
     t.part_bytes = B * t.it * t.jt * H * rows * 4;
     return t;
@@ -681,9 +683,9 @@ int run_relpos_bwd(int dev, evo::RelParams<T> p, const void* dpair, void* dtable
     auto kernel = vec ? (chains ? evo::evo_relpos_bwd_kernel<T, true, true> : evo::evo_relpos_bwd_kernel<T, true, false>)
                       : (chains ? evo::evo_relpos_bwd_kernel<T, false, true> : evo::evo_relpos_bwd_kernel<T, false, false>);
     static AttrOnce attrs[4];
-    if (!attrs[2 * vec + chains].ensure(dev, kernel, evo::rel_smem(evo::kRelBins * evo::kRelBwdThreads * 4, evo::kRelMaxBorders)))
+    if (!attrs[2 * vec + chains].ensure(dev, kernel, evo::rel_bwd_smem(evo::kRelBins, evo::kRelMaxBorders)))
         return EVO_ERR_CUDA;
-    const int smem = evo::rel_smem(std::min(p.rows, evo::kRelBins) * evo::kRelBwdThreads * 4, p.nb);
+    const int smem = evo::rel_bwd_smem(std::min(p.rows, evo::kRelBins), p.nb);
     const dim3 grid{unsigned(t.jt), unsigned(t.it), unsigned(p.B * p.H * t.chunks)};
     if (!launch(kernel, grid, evo::kRelBwdThreads, smem, st, p)) return EVO_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -777,7 +779,8 @@ extern "C" EVO_API int evo_relpos_bwd(const void* dpair, const int32_t* borders,
     }
     if (!dpair || (!borders && num_borders > 0) || !pos_q || !pos_k || !workspace) return EVO_ERR_INVALID_ARG;
     const RelTiles t = rel_bwd_tiles(B, Sq, Sk, H, rows);
-    if (B * H * t.chunks > 65535) return EVO_ERR_UNSUPPORTED_SHAPE;
+    // blocks of the grid's z dimension; element offsets inside a tile are 32-bit
+    if (B * H * t.chunks > 65535 || int64_t(t.ti) * Sk > kIntMax) return EVO_ERR_UNSUPPORTED_SHAPE;
     if (workspace_bytes < t.part_bytes) return EVO_ERR_INVALID_ARG;
     if (!aligned(dpair, uintptr_t(es)) || !aligned(workspace, 256)) return EVO_ERR_MISALIGNED;
     for (const int32_t* p : {borders, pos_q, pos_k, chain_q, chain_k})

@@ -229,42 +229,58 @@ __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const Re
 // is fixed.  While no column of a warp leaves its bucket the sums stay in
 // registers; when one does, the warp adds all of them to their bins, without a
 // branch for each (branches for each column, or taking only the columns that
-// moved, cost 5 times as much: near the diagonal most rows move some column).
-// The next row's values are in flight meanwhile.  VEC: a thread's columns are
-// runs of 16 whole bytes; else they lie the block's width apart.
+// moved, took 5 times as long: near the diagonal most rows move some column).
+// The next two rows' values are in flight meanwhile.  The issue rate is the limit
+// beside the memory, so the distance table holds the bins' byte offsets (a row of
+// another range of bins: the one behind the last, which nobody reads) and the
+// positions are kept as byte offsets into it: an element costs a subtraction, a
+// clamp, a read and an addition.  That needs positions below 2^27 in size and
+// borders within the table's span; other blocks search the borders.
+// VEC: a thread's columns are runs of 16 whole bytes; else they lie the block's
+// width apart.
+__host__ __device__ inline int rel_bwd_smem(int bins, int nb) {
+    return (bins + 1) * kRelBwdThreads * 4 + (nb + 3) / 4 * 16 + kRelLut * 4;
+}
+
 template <typename T, bool VEC, bool CHAINS>
 __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const RelParams<T> p) {
     constexpr int RUN = VEC ? 16 / int(sizeof(T)) : 1;  // adjacent columns
     constexpr int COLS = kRelBwdCols;
+    constexpr int ROW = kRelBwdThreads * 4;  // bytes of a bin
     extern __shared__ __align__(16) uint8_t rel_sm[];
     const int jt = blockIdx.x, itile = blockIdx.y;
     const int chunks = (p.rows + kRelBins - 1) / kRelBins;
     const int bin0 = (blockIdx.z % chunks) * kRelBins, nbins = min(kRelBins, p.rows - bin0);
     const int bh = blockIdx.z / chunks, b = bh / p.H, h = bh % p.H;
-    float* bins = reinterpret_cast<float*>(rel_sm);  // [nbins][128]
-    int* sborders = reinterpret_cast<int*>(bins + min(p.rows, kRelBins) * kRelBwdThreads);
-    uint16_t* lut = reinterpret_cast<uint16_t*>(sborders + (p.nb + 3) / 4 * 4);
-    for (int i = threadIdx.x; i < nbins * (kRelBwdThreads / 4); i += kRelBwdThreads)
+    float* bins = reinterpret_cast<float*>(rel_sm);  // [nbins + 1][128]
+    int* sborders = reinterpret_cast<int*>(bins + (min(p.rows, kRelBins) + 1) * kRelBwdThreads);
+    uint32_t* lut = reinterpret_cast<uint32_t*>(sborders + (p.nb + 3) / 4 * 4);
+    for (int i = threadIdx.x; i < (nbins + 1) * (kRelBwdThreads / 4); i += kRelBwdThreads)
         reinterpret_cast<float4*>(bins)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = threadIdx.x; i < p.nb; i += kRelBwdThreads) sborders[i] = p.borders[i];
+
     const int lanes = 1 << p.lane_cols, tx = threadIdx.x & (lanes - 1), ty = threadIdx.x >> p.lane_cols;
-    const int j0 = jt * lanes * COLS + tx * RUN, i_end = min(p.Sq, (itile + 1) * p.ti), di = kRelBwdThreads >> p.lane_cols;
+    const int i0 = itile * p.ti, rows = min(p.Sq - i0, p.ti), di = kRelBwdThreads >> p.lane_cols;
+    const int j0 = jt * lanes * COLS + tx * RUN;
     auto col = [&](int e) -> int { return j0 + (e / RUN) * lanes * RUN + e % RUN; };
+    const T* tile = p.dpair + ((long long)bh * p.Sq + i0) * p.Sk;  // row i of the tile: 32-bit offsets (ti * Sk < 2^31)
+    const int *posq = p.pos_q + (long long)b * p.Sq + i0, *chainq = CHAINS ? p.chain_q + (long long)b * p.Sq + i0 : nullptr;
     constexpr int WORDS = VEC ? COLS * int(sizeof(T)) / 4 : COLS;  // a row's values as loaded
-    auto fetch = [&](int i, uint32_t (&w)[WORDS]) {
-        const T* row = p.dpair + ((long long)bh * p.Sq + i) * p.Sk;
+    auto fetch = [&](int i, uint32_t (&w)[WORDS]) {  // row i, or the last one once more
+        const uint32_t at = uint32_t(min(i, rows - 1)) * uint32_t(p.Sk);
         if constexpr (VEC) {
 #pragma unroll
             for (int k = 0; k < WORDS / 4; ++k) {
                 const int j = col(k * RUN);
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (i < i_end && j < p.Sk) x = *reinterpret_cast<const uint4*>(row + j);
+                if (j < p.Sk) x = *reinterpret_cast<const uint4*>(tile + (at + uint32_t(j)));
                 w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
             }
         } else {
 #pragma unroll
             for (int e = 0; e < COLS; ++e) {
                 const int j = col(e);
-                w[e] = i < i_end && j < p.Sk ? __float_as_uint(rel_f32(row[j])) : 0u;
+                w[e] = j < p.Sk ? __float_as_uint(rel_f32(tile[at + uint32_t(j)])) : 0u;
             }
         }
     };
@@ -273,43 +289,68 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
         else if constexpr (std::is_same<T, __half>::value) return __half2float(reinterpret_cast<const __half*>(w)[e]);
         else return e & 1 ? ptx::bf16hi_to_f32(w[e / 2]) : ptx::bf16lo_to_f32(w[e / 2]);
     };
-    uint32_t w[WORDS], next[WORDS];
-    int i = itile * p.ti + ty;
-    fetch(i, w);
-    int pk[COLS], ck[COLS], cur[COLS];
-    float sum[COLS];
+    uint32_t w[WORDS], next[WORDS], after[WORDS];
+    fetch(ty, w);
+    fetch(ty + di, next);
+    int pk[COLS], ck[COLS];
+    bool near = true;
+    auto small = [](int v) { return v > -(1 << 27) && v < (1 << 27); };
 #pragma unroll
     for (int e = 0; e < COLS; ++e) {
         const int j = col(e);
         pk[e] = j < p.Sk ? p.pos_k[(long long)b * p.Sk + j] : 0;
         ck[e] = CHAINS && j < p.Sk ? p.chain_k[(long long)b * p.Sk + j] : 0;
-        cur[e] = -1;
+        near = near && small(pk[e]);
+    }
+    for (int i = threadIdx.x; i < rows; i += kRelBwdThreads) near = near && small(posq[i]);
+    near = __syncthreads_and(near);  // also: the borders are in place
+
+    RelLookup L;
+    L.borders = sborders;
+    L.nb = p.nb;
+    auto offset = [&](int r) -> uint32_t { return min(uint32_t(r - bin0), uint32_t(nbins)) * ROW; };
+    // one entry below the first border, one for each distance up to the last
+    const long long first = p.nb > 0 ? sborders[0] : 0, last = p.nb > 0 ? sborders[p.nb - 1] : 0;
+    const long long span = last - first + 2;
+    const bool direct = near && span >= 2 && span <= kRelLut && small(int(first)) && small(int(last));
+    if (direct)
+        for (int e = threadIdx.x; e < int(span); e += kRelBwdThreads) lut[e] = offset(L.search(int(first) - 1 + e));
+    __syncthreads();
+    const int limit = 4 * int(span) - 4;  // byte offset of the last entry
+    if (direct) {
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) pk[e] = 4 * (pk[e] + int(first) - 1);
+    }
+
+    char* mine = reinterpret_cast<char*>(bins + threadIdx.x);
+    auto flush = [&](uint32_t at, float s) { *reinterpret_cast<float*>(mine + at) += s; };
+    uint32_t cur[COLS];
+    float sum[COLS];
+#pragma unroll
+    for (int e = 0; e < COLS; ++e) {
+        cur[e] = uint32_t(nbins) * ROW;
         sum[e] = 0.0f;
     }
-    const RelLookup L = rel_setup(p.borders, p.nb, sborders, lut);
-    float* mine = bins + threadIdx.x;
-    auto flush = [&](int r, float s) {
-        if (unsigned(r - bin0) < unsigned(nbins)) mine[(r - bin0) * kRelBwdThreads] += s;
-    };
-    for (; i < i_end; i += di) {
-        fetch(i + di, next);
-        const int pq = p.pos_q[(long long)b * p.Sq + i];
-        const int cq = CHAINS ? p.chain_q[(long long)b * p.Sq + i] : 0;
-        int r[COLS];
-        bool moved = false;
-        if (L.direct) {
+    const uint32_t apart = offset(p.nb + 1);
+    int pq = ty < rows ? posq[ty] : 0, cq = CHAINS && ty < rows ? chainq[ty] : 0;
+    for (int i = ty; i < rows; i += di) {
+        fetch(i + 2 * di, after);
+        const int pq_next = posq[min(i + di, rows - 1)], cq_next = CHAINS ? chainq[min(i + di, rows - 1)] : 0;
+        uint32_t r[COLS], moved = 0;
+        if (direct) {
 #pragma unroll
-            for (int e = 0; e < COLS; ++e) r[e] = L.lut[min(max(rel_distance(pq, pk[e]), L.lo), L.last) - L.lo];
+            for (int e = 0; e < COLS; ++e)
+                r[e] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(lut) + __vimin_s32_relu(4 * pq - pk[e], limit));
         } else {
 #pragma unroll
-            for (int e = 0; e < COLS; ++e) r[e] = L.search(rel_distance(pq, pk[e]));
+            for (int e = 0; e < COLS; ++e) r[e] = offset(L.search(rel_distance(pq, pk[e])));
         }
 #pragma unroll
         for (int e = 0; e < COLS; ++e) {
-            if (CHAINS && cq != ck[e]) r[e] = p.nb + 1;
-            moved |= r[e] != cur[e];
+            if (CHAINS && cq != ck[e]) r[e] = apart;
+            moved |= r[e] ^ cur[e];
         }
-        if (__any_sync(__activemask(), moved)) {
+        if (__any_sync(__activemask(), moved != 0)) {
 #pragma unroll
             for (int e = 0; e < COLS; ++e) {
                 flush(cur[e], sum[e]);
@@ -321,21 +362,23 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
             for (int e = 0; e < COLS; ++e) sum[e] += value(w, e);
         }
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) w[k] = next[k];
+        for (int k = 0; k < WORDS; ++k) w[k] = next[k], next[k] = after[k];
+        pq = pq_next;
+        cq = cq_next;
     }
 #pragma unroll
     for (int e = 0; e < COLS; ++e) flush(cur[e], sum[e]);
     __syncthreads();
     // the 128 columns of each bin, a warp a bin, in a fixed order
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long tile = ((long long)b * gridDim.y + itile) * gridDim.x + jt;
+    const long long slot = ((long long)b * gridDim.y + itile) * gridDim.x + jt;
 #pragma unroll 4
     for (int r = warp; r < nbins; r += kRelBwdThreads / 32) {
         const float4 x = reinterpret_cast<const float4*>(bins + r * kRelBwdThreads)[lane];
         float s = (x.x + x.y) + (x.z + x.w);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) p.part[(tile * p.H + h) * p.rows + bin0 + r] = s;
+        if (lane == 0) p.part[(slot * p.H + h) * p.rows + bin0 + r] = s;
     }
 }
 
