@@ -62,7 +62,7 @@ def test_both_activations(act, dt):
 
 def test_more_rows_than_one_chunk():
     """Rows are taken in chunks; the weight gradients add up over them."""
-    M, C, F = 2 * 18944 + 300, 16, 1200
+    M, C, F = 4 * 18944 + 300, 16, 1200
     assert evo.evo_transition_bwd_workspace_size(M, C, F, evo.EVO_DTYPE_BF16) == \
         evo.evo_transition_bwd_workspace_size(M + 18944, C, F, evo.EVO_DTYPE_BF16)
     check(*make(M, C, F, BF16, seed=1), "silu", f"chunks {M}")

@@ -68,13 +68,15 @@ int select_device(std::initializer_list<const void*> ptrs, DeviceScope& scope) {
 
 // ------------------------------------------------------------------ transition
 
-// Rows are taken in chunks whose [rows, F] intermediates stay in the 126 MB L2
-// between the kernel that writes them and the ones that read them, and bound
-// the workspace.  A chunk is a whole number of 128-row tiles for each of 148 SMs.
+// Rows are taken in chunks, which bound the workspace: forward ones so that the
+// [rows, F] intermediate stays in the 126 MB L2 between the kernel that writes it
+// and the one that reads it, backward ones of 512 MB, because every chunk adds to
+// the partial weight gradients once.  A chunk is a whole number of 128-row tiles
+// for each of 148 SMs.
 constexpr int64_t kTrWave = 148 * 128;
 
-int64_t tr_chunk_rows(int64_t M, int64_t row_bytes) {
-    const int64_t target = int64_t(64) << 20;
+int64_t tr_chunk_rows(int64_t M, int64_t row_bytes, bool backward) {
+    const int64_t target = int64_t(backward ? 512 : 64) << 20;
     const int64_t waves = std::max<int64_t>(1, target / (kTrWave * std::max<int64_t>(row_bytes, 1)));
     return std::min(M, waves * kTrWave);
 }
@@ -84,7 +86,8 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 struct TrLayout {
     int64_t chunk = 0;                            // rows of a chunk
     int64_t h = 0, dg = 0, du = 0;                // [chunk, F] (16-bit: rows up to 128, F up to 128)
-    int64_t part = 0;                             // partial weight gradients, fp32
+    int64_t part = 0, part2 = 0, part3 = 0;       // partial weight gradients, fp32: [splits][R][N up to 4] (fp32 call: one)
+    bool direct = false;                          // 16-bit: the last products are the weight gradients
     int64_t splits = 0, split_rows = 0;           // ranges of rows with a slot of their own
     bool fused = false;                           // the forward's one-kernel form: no [M, F] array at all
     int64_t x = 0, dy = 0, wg = 0, wu = 0, wd = 0;  // 16-bit, odd C or F: copies with rows of whole 16-byte units
@@ -105,8 +108,8 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
     L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
     L->fused = !backward && tr_fused(M, C, dtype);
     // (the one-kernel forward needs chunks only for the copy of X)
-    L->chunk = L->fused ? (L->pad ? tr_chunk_rows(M, round_up(C, 8) * 2) : M)
-                        : tr_chunk_rows(M, ldf * es * (backward ? 3 : 1));
+    L->chunk = L->fused ? (L->pad ? tr_chunk_rows(M, round_up(C, 8) * 2, false) : M)
+                        : tr_chunk_rows(M, ldf * es * (backward ? 3 : 1), backward);
     const int64_t hbytes = (dtype == EVO_DTYPE_FP32 ? L->chunk : round_up(L->chunk, 128)) * ldf * es;
     int64_t off = 0;
     auto take = [&off](int64_t bytes) {
@@ -126,10 +129,17 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
             L->part = take(L->splits * 3 * fc * 4);
         } else {
             // as many ranges as keep the tiles within one wave of 148 SMs, none under 512 rows
-            const int64_t tiles = 3 * ((F + 255) / 256) * ((C + 127) / 128);
+            const int64_t bn = C > 128 ? 256 : 128;
+            const int64_t tiles = 2 * ((F + 127) / 128) * ((C + bn - 1) / bn) + ((C + 127) / 128) * ((F + 255) / 256);
             L->splits = std::max<int64_t>(1, std::min(148 / tiles, (L->chunk + 511) / 512));
             L->split_rows = round_up((L->chunk + L->splits - 1) / L->splits, 64);
-            L->part = take(L->splits * 3 * round_up(C, 128) * round_up(F, 256) * 4);
+            L->direct = L->splits == 1 && L->chunk == M && !L->pad;
+            if (!L->direct) {
+                const int64_t fc4 = F * round_up(C, 4) * 4;
+                L->part = take(L->splits * fc4);
+                L->part2 = take(L->splits * fc4);
+                L->part3 = take(L->splits * C * round_up(F, 4) * 4);
+            }
         }
     }
     if (L->pad) {
@@ -260,7 +270,8 @@ int launch_mma(int dev, int sms, const evo::TrMaps& maps, const evo::TrMmaParams
     static AttrOnce attr;
     if (!attr.ensure(dev, kernel, Cfg::SMEM_BYTES)) return EVO_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min(p.num_tiles, sms)), 1, 1);
+    const int tiles = KIND == evo::TR_DW ? p.num_tiles * p.tiles_n : p.num_tiles;
+    cfg.gridDim = dim3(unsigned(std::min(tiles, sms)), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = st;
@@ -274,43 +285,63 @@ struct TrSource {
     int64_t ldc, ldf;  // row strides of x, dy, wg, wu and of wd
 };
 
-bool pad_rows(const void* src, void* dst, int64_t rows, int64_t w, int64_t wp, int sms, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min<int64_t>((rows * w + 1023) / 1024, int64_t(sms) * 8)), 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, evo::evo_tr_pad_kernel, static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst),
-                              (long long)rows, int(w), int(wp)) == cudaSuccess;
+struct PadList {
+    evo::TrPads p = {};
+    void add(const void* src, void* dst, int64_t rows, int64_t w) {
+        p.src[p.n] = static_cast<const uint16_t*>(src);
+        p.dst[p.n] = static_cast<uint16_t*>(dst);
+        p.rows[p.n] = int(rows);
+        p.w[p.n] = int(w);
+        p.wp[p.n++] = int(round_up(w, 8));
+    }
+    bool run(int sms, cudaStream_t st) {
+        int64_t rows = 0;
+        for (int k = 0; k < p.n; ++k) rows += p.rows[k];
+        return launch(evo::evo_tr_pad_kernel, dim3(unsigned(std::min<int64_t>((rows + 7) / 8, int64_t(sms) * 8))), 256, 0, st, p);
+    }
+};
+
+// Copies of the chunk's rows of x and dy and, with the first chunk, of the weights.
+bool pad_chunk(const TrLayout& L, char* ws, TrSource* s, const void** x, const void** dy, int64_t rows, bool weights,
+               int64_t C, int64_t F, int sms, cudaStream_t st) {
+    PadList list;
+    list.add(*x, ws + L.x, rows, C);
+    *x = ws + L.x;
+    if (dy) {
+        list.add(*dy, ws + L.dy, rows, C);
+        *dy = ws + L.dy;
+    }
+    if (weights) {
+        list.add(s->wg, ws + L.wg, F, C);
+        list.add(s->wu, ws + L.wu, F, C);
+        list.add(s->wd, ws + L.wd, C, F);
+        s->wg = ws + L.wg;
+        s->wu = ws + L.wu;
+        s->wd = ws + L.wd;
+        s->ldc = round_up(C, 8);
+        s->ldf = round_up(F, 8);
+    }
+    return list.run(sms, st);
 }
 
-int pad_weights(const TrLayout& L, char* ws, TrSource* s, int64_t C, int64_t F, int sms, cudaStream_t st) {
-    s->ldc = round_up(C, 8);
-    s->ldf = round_up(F, 8);
-    if (!pad_rows(s->wg, ws + L.wg, F, C, s->ldc, sms, st) || !pad_rows(s->wu, ws + L.wu, F, C, s->ldc, sms, st) ||
-        !pad_rows(s->wd, ws + L.wd, C, F, s->ldf, sms, st))
-        return EVO_ERR_CUDA;
-    s->wg = ws + L.wg;
-    s->wu = ws + L.wu;
-    s->wd = ws + L.wd;
-    return EVO_OK;
-}
-
-// Widest stores that rows of C 16-bit elements from `p` allow.
-int wide_store(const void* p, int64_t C) {
-    return C % 16 == 0 && aligned(p, 32) ? 2 : C % 8 == 0 && aligned(p, 16) ? 1 : 0;
-}
+// Whether TMA can store rows of C 16-bit elements at p.
+bool tma_rows(const void* p, int64_t C) { return C % 8 == 0 && aligned(p, 16); }
 
 int tiles_of(int64_t n, int64_t tile) { return int((n + tile - 1) / tile); }
 
-// Y or dX of one chunk: 256 channels a tile where there are more than 128.
+// Y or dX of one chunk: 256 channels a tile where there are more than 128 and
+// tiles enough for the SMs.
 template <int KIND, bool F16>
-int launch_out(int dev, int sms, const evo::TrMaps& maps, evo::TrMmaParams p, cudaStream_t st) {
+int launch_out(int dev, int sms, evo::TrMaps& maps, evo::TrMmaParams p, void* out, cudaStream_t st) {
+    p.out = static_cast<uint16_t*>(out);
+    p.tma_out = tma_rows(out, p.C);
+    if (p.tma_out && !encode_rows(&maps.m[KIND == evo::TR_OUT ? 2 : 4], out, p.rows, p.C, p.C, 32, F16, 32)) return EVO_ERR_CUDA;
     p.tiles_m = tiles_of(p.rows, 128);
-    p.tiles_n = tiles_of(p.C, p.C > 128 ? 256 : 128);
+    const bool wide = p.C > 128 && p.tiles_m * tiles_of(p.C, 128) > sms;
+    p.tiles_n = tiles_of(p.C, wide ? 256 : 128);
     p.num_tiles = p.tiles_m * p.tiles_n;
     p.kb = tiles_of(p.F, 64);
-    return p.C > 128 ? launch_mma<KIND, 0, F16, 256>(dev, sms, maps, p, st)
-                     : launch_mma<KIND, 0, F16, 128>(dev, sms, maps, p, st);
+    return wide ? launch_mma<KIND, 0, F16, 256>(dev, sms, maps, p, st) : launch_mma<KIND, 0, F16, 128>(dev, sms, maps, p, st);
 }
 
 template <int ACT, bool F16, int CN>
@@ -351,25 +382,18 @@ int run_fwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
     TrLayout L;
     tr_layout(M, C, F, dtype, false, &L);
     TrSource s = {X, nullptr, Wg, Wu, Wd, C, F};
-    if (L.pad && pad_weights(L, ws, &s, C, F, sms, st) != EVO_OK) return EVO_ERR_CUDA;
     evo::TrMmaParams p = {};
     p.C = int(C);
     p.F = int(F);
-    p.h = reinterpret_cast<uint16_t*>(ws + L.h);
-    p.ldf = int(round_up(F, 128));
-    p.wide_store = wide_store(Y, C);
+    const int64_t ldf = round_up(F, 128);
     for (int64_t m = 0; m < M; m += L.chunk) {
         p.rows = int(std::min(L.chunk, M - m));
-        const char* x = static_cast<const char*>(X) + m * C * 2;
-        if (L.pad) {
-            if (!pad_rows(x, ws + L.x, p.rows, C, s.ldc, sms, st)) return EVO_ERR_CUDA;
-            x = ws + L.x;
-        }
+        const void* x = static_cast<const char*>(X) + m * C * 2;
+        uint16_t* y = static_cast<uint16_t*>(Y) + m * C;
+        if (L.pad && !pad_chunk(L, ws, &s, &x, nullptr, p.rows, m == 0, C, F, sms, st)) return EVO_ERR_CUDA;
         if (L.fused) {
-            const int fst = C > 128 ? launch_fused<ACT, F16, 256>(dev, sms, x, s, static_cast<uint16_t*>(Y) + m * C, p.rows,
-                                                                  C, F, p.wide_store, st)
-                                    : launch_fused<ACT, F16, 128>(dev, sms, x, s, static_cast<uint16_t*>(Y) + m * C, p.rows,
-                                                                  C, F, p.wide_store, st);
+            const int fst = C > 128 ? launch_fused<ACT, F16, 256>(dev, sms, x, s, y, p.rows, C, F, tma_rows(y, C), st)
+                                    : launch_fused<ACT, F16, 128>(dev, sms, x, s, y, p.rows, C, F, tma_rows(y, C), st);
             if (fst != EVO_OK) return fst;
             continue;
         }
@@ -378,17 +402,31 @@ int run_fwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
         std::memset(&out, 0, sizeof(out));
         if (!encode_rows(&gate.m[0], x, p.rows, C, s.ldc, 128, F16) || !encode_rows(&gate.m[1], s.wg, F, C, s.ldc, 128, F16) ||
             !encode_rows(&gate.m[2], s.wu, F, C, s.ldc, 128, F16) ||
-            !encode_rows(&out.m[0], p.h, p.rows, F, p.ldf, 128, F16) || !encode_rows(&out.m[1], s.wd, C, F, s.ldf, 128, F16))
+            !encode_rows(&gate.m[3], ws + L.h, p.rows, ldf, ldf, 32, F16, 32) ||
+            !encode_rows(&out.m[0], ws + L.h, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[1], s.wd, C, F, s.ldf, 128, F16))
             return EVO_ERR_CUDA;
         p.tiles_m = tiles_of(p.rows, 128);
         p.tiles_n = tiles_of(F, 128);
         p.num_tiles = p.tiles_m * p.tiles_n;
         p.kb = tiles_of(C, 64);
-        if (launch_mma<evo::TR_GATE, ACT, F16, 256>(dev, sms, gate, p, st) != EVO_OK) return EVO_ERR_CUDA;
-        p.out = static_cast<uint16_t*>(Y) + m * C;
-        if (launch_out<evo::TR_OUT, F16>(dev, sms, out, p, st) != EVO_OK) return EVO_ERR_CUDA;
+        if (launch_mma<evo::TR_GATE, ACT, F16, 256>(dev, sms, gate, p, st) != EVO_OK ||
+            launch_out<evo::TR_OUT, F16>(dev, sms, out, p, y, st) != EVO_OK)
+            return EVO_ERR_CUDA;
     }
     return EVO_OK;
+}
+
+// The slots of one weight gradient as a 3-D tensor {N, R, splits} of fp32; a box
+// is 32 columns (128 B rows, 128 B swizzle) of 32 rows.
+bool encode_slots(CUtensorMap* m, void* base, int64_t splits, int64_t R, int64_t N) {
+    const int64_t ld = round_up(N, 4);
+    const cuuint64_t dims[3] = {cuuint64_t(N), cuuint64_t(R), cuuint64_t(splits)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld * 4), cuuint64_t(R * ld * 4)};
+    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool F16, int ACT>
@@ -400,67 +438,76 @@ int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
     TrLayout L;
     tr_layout(M, C, F, dtype, true, &L);
     TrSource s = {X, dY, Wg, Wu, Wd, C, F};
-    if (L.pad && pad_weights(L, ws, &s, C, F, sms, st) != EVO_OK) return EVO_ERR_CUDA;
     evo::TrMmaParams p = {};
     p.C = int(C);
     p.F = int(F);
-    p.h = reinterpret_cast<uint16_t*>(ws + L.h);
-    p.dg = reinterpret_cast<uint16_t*>(ws + L.dg);
-    p.du = reinterpret_cast<uint16_t*>(ws + L.du);
-    p.part = reinterpret_cast<float*>(ws + L.part);
-    p.ldf = int(round_up(F, 128));
-    p.ldc = int(round_up(C, 128));
-    p.ldf2 = int(round_up(F, 256));
+    const int64_t ldf = round_up(F, 128);
     p.split_rows = int(L.split_rows);
+    p.direct = L.direct;
+    p.bn01 = C > 128 ? 256 : 128;
+    p.tn01 = tiles_of(C, p.bn01);
+    p.tn2 = tiles_of(F, 256);
+    p.tiles01 = p.tn01 * tiles_of(F, 128);
+    p.tiles2 = p.tn2 * tiles_of(C, 128);
     void* const dw[3] = {dWg, dWu, dWd};
+    char* const part[3] = {ws + L.part, ws + L.part2, ws + L.part3};
+    int dw_tiles = 0;
     for (int w = 0; w < 3; ++w)
-        if (dw[w]) p.which[p.num_which++] = w;
-    p.wide_store = dX ? wide_store(dX, C) : 0;
+        if (dw[w]) {
+            p.which[p.num_which++] = w;
+            dw_tiles += w == 2 ? p.tiles2 : p.tiles01;
+        }
     for (int64_t m = 0; m < M; m += L.chunk) {
         p.rows = int(std::min(L.chunk, M - m));
         p.first = m == 0;
-        const char* x = static_cast<const char*>(X) + m * C * 2;
-        const char* dy = static_cast<const char*>(dY) + m * C * 2;
-        if (L.pad) {
-            if (!pad_rows(x, ws + L.x, p.rows, C, s.ldc, sms, st) || !pad_rows(dy, ws + L.dy, p.rows, C, s.ldc, sms, st))
-                return EVO_ERR_CUDA;
-            x = ws + L.x;
-            dy = ws + L.dy;
-        }
+        const void* x = static_cast<const char*>(X) + m * C * 2;
+        const void* dy = static_cast<const char*>(dY) + m * C * 2;
+        if (L.pad && !pad_chunk(L, ws, &s, &x, &dy, p.rows, m == 0, C, F, sms, st)) return EVO_ERR_CUDA;
+        char *h = ws + L.h, *dg = ws + L.dg, *du = ws + L.du;
         evo::TrMaps grad, out, wgt;
         std::memset(&out, 0, sizeof(out));
+        std::memset(&wgt, 0, sizeof(wgt));
         if (!encode_rows(&grad.m[0], x, p.rows, C, s.ldc, 128, F16) || !encode_rows(&grad.m[1], s.wg, F, C, s.ldc, 128, F16) ||
             !encode_rows(&grad.m[2], s.wu, F, C, s.ldc, 128, F16) || !encode_rows(&grad.m[3], dy, p.rows, C, s.ldc, 128, F16) ||
-            !encode_rows(&grad.m[4], s.wd, C, F, s.ldf, 64, F16) ||
-            !encode_rows(&out.m[0], p.dg, p.rows, F, p.ldf, 128, F16) || !encode_rows(&out.m[1], s.wg, F, C, s.ldc, 64, F16) ||
-            !encode_rows(&out.m[2], p.du, p.rows, F, p.ldf, 128, F16) || !encode_rows(&out.m[3], s.wu, F, C, s.ldc, 64, F16) ||
+            !encode_rows(&grad.m[4], s.wd, C, F, s.ldf, 64, F16) || !encode_rows(&grad.m[5], h, p.rows, ldf, ldf, 32, F16, 32) ||
+            !encode_rows(&grad.m[6], dg, p.rows, ldf, ldf, 32, F16, 32) || !encode_rows(&grad.m[7], du, p.rows, ldf, ldf, 32, F16, 32) ||
+            !encode_rows(&out.m[0], dg, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[1], s.wg, F, C, s.ldc, 64, F16) ||
+            !encode_rows(&out.m[2], du, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[3], s.wu, F, C, s.ldc, 64, F16) ||
             !encode_rows(&wgt.m[0], x, p.rows, C, s.ldc, 64, F16) || !encode_rows(&wgt.m[1], dy, p.rows, C, s.ldc, 64, F16) ||
-            !encode_rows(&wgt.m[2], p.dg, p.rows, F, p.ldf, 64, F16) || !encode_rows(&wgt.m[3], p.du, p.rows, F, p.ldf, 64, F16) ||
-            !encode_rows(&wgt.m[4], p.h, p.rows, F, p.ldf, 64, F16))
+            !encode_rows(&wgt.m[2], dg, p.rows, ldf, ldf, 64, F16) || !encode_rows(&wgt.m[3], du, p.rows, ldf, ldf, 64, F16) ||
+            !encode_rows(&wgt.m[4], h, p.rows, ldf, ldf, 64, F16))
             return EVO_ERR_CUDA;
+        for (int w = 0; w < 3; ++w) {
+            const int64_t R = w == 2 ? C : F, N = w == 2 ? F : C;
+            if (dw[w] && !(L.direct ? encode_rows(&wgt.m[5 + w], dw[w], R, N, N, 32, F16, 32)
+                                    : encode_slots(&wgt.m[5 + w], part[w], L.splits, R, N)))
+                return EVO_ERR_CUDA;
+        }
         p.tiles_m = tiles_of(p.rows, 128);
         p.tiles_n = tiles_of(F, 128);
         p.num_tiles = p.tiles_m * p.tiles_n;
         p.kb = tiles_of(C, 64);
         if (launch_mma<evo::TR_GRAD, ACT, F16, 256>(dev, sms, grad, p, st) != EVO_OK) return EVO_ERR_CUDA;
-        if (dX) {
-            p.out = static_cast<uint16_t*>(dX) + m * C;
-            if (launch_out<evo::TR_DX, F16>(dev, sms, out, p, st) != EVO_OK) return EVO_ERR_CUDA;
-        }
+        if (dX && launch_out<evo::TR_DX, F16>(dev, sms, out, p, static_cast<uint16_t*>(dX) + m * C, st) != EVO_OK)
+            return EVO_ERR_CUDA;
         if (p.num_which > 0) {
-            p.tiles_m = tiles_of(C, 128);
-            p.tiles_n = tiles_of(F, 256);
-            p.num_tiles = int(p.num_which * p.tiles_m * p.tiles_n * L.splits);
+            p.num_tiles = dw_tiles;
+            p.tiles_n = int(L.splits);
             if (launch_mma<evo::TR_DW, 0, F16, 256>(dev, sms, wgt, p, st) != EVO_OK) return EVO_ERR_CUDA;
         }
     }
-    if (p.num_which > 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(blocks_of(F, 32), blocks_of(C, 32), 3);
-        cfg.blockDim = dim3(256, 1, 1);
-        cfg.stream = st;
-        if (cudaLaunchKernelEx(&cfg, evo::evo_tr_mma_reduce_kernel<T>, (const float*)p.part, int(L.splits), p.C, p.F, p.ldc,
-                               p.ldf2, static_cast<T*>(dWg), static_cast<T*>(dWu), static_cast<T*>(dWd)) != cudaSuccess)
+    if (p.num_which > 0 && !L.direct) {
+        evo::TrReduceParams<T> r = {};
+        r.splits = int(L.splits);
+        for (int w = 0; w < 3; ++w) {
+            r.part[w] = reinterpret_cast<const float*>(part[w]);
+            r.out[w] = static_cast<T*>(dw[w]);
+            r.R[w] = int(w == 2 ? C : F);
+            r.N[w] = int(w == 2 ? F : C);
+            r.ld[w] = int(round_up(r.N[w], 4));
+        }
+        const int64_t big = std::max(C, F);
+        if (!launch(evo::evo_tr_mma_reduce_kernel<T>, dim3(blocks_of(big, 4), blocks_of(big, 256), 3), 256, 0, st, r))
             return EVO_ERR_CUDA;
     }
     return EVO_OK;

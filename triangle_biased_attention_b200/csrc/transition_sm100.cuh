@@ -14,16 +14,19 @@
 //         runs during this tile's epilogue.
 //   DX    dX = dG Wg + dU Wu             128 rows x BN channels, both products
 //         into one accumulator
-//   DW    [X^T dG, X^T dU, dY^T H], [C, F] each: 128 channels x 256 features of
-//         one range of rows, summed into the range's own fp32 slot.
+//   DW    dG^T X, dU^T X [F, C] and dY^T H [C, F]: 128 x 256 (or 128 x 128) of one
+//         range of rows, written as the gradient itself where one range takes all
+//         rows, else added into the range's own fp32 slot.
 // Operands that are contiguous along k are read K-major, the others (Wd in GRAD,
 // the weights in DX, both in DW) MN-major: the same swizzled TMA boxes of 128-byte
 // rows serve both, so nothing is transposed in memory.
 //
 // Warp roles (384 threads): warp 0 loads (TMA ring), warp 1 issues the MMAs,
 // warps 4-11 drain the accumulators: warp w reads the 32 tensor-memory lanes of
-// its place in its warpgroup, the two warpgroups half the columns each.  Stores
-// go straight from registers, 32 whole bytes a thread.
+// its place in its warpgroup, the two warpgroups half the columns each.  Results
+// leave through 32-column boxes of shared memory, a warp's own, and TMA stores:
+// stored from registers a warp writes 32 rows 16 or 32 bytes at a time, which took
+// longer than the products (GRAD at C = 128: 22 us for 18944 rows x 512 features).
 // Every wait is bounded (2 s); on expiry the CTA records EVO_ERR_TIMEOUT, drains
 // its own copies and MMAs, frees tensor memory and exits.
 #pragma once
@@ -38,35 +41,39 @@ namespace evo {
 
 enum TrKind { TR_GATE, TR_OUT, TR_GRAD, TR_DX, TR_DW };
 
-// GATE: X, Wg, Wu.  OUT: H, Wd.  GRAD: X, Wg, Wu, dY, Wd.  DX: dG, Wg, dU, Wu.
-// DW: X, dY, dG, dU, H.
+// Operands, then results (0-based): GATE: X, Wg, Wu, H.  OUT: H, Wd, Y.
+// GRAD: X, Wg, Wu, dY, Wd, H, dG, dU.  DX: dG, Wg, dU, Wu, dX.
+// DW: X, dY, dG, dU, H, and the three gradients (or their slots).
 struct TrMaps {
-    CUtensorMap m[5];
+    CUtensorMap m[8];
 };
 
 struct TrMmaParams {
-    uint16_t *h, *dg, *du;  // [rows up to 128, ldf]
-    uint16_t* out;          // Y or dX, [rows, C]
-    float* part;            // DW: [splits][3][ldc][ldf2]
+    uint16_t* out;    // Y or dX, [rows, C]
     int rows, C, F;
-    int ldf;                // row stride of h, dg, du: F rounded up to 128
-    int ldc, ldf2;          // rows and row stride of a slot: C up to 128, F up to 256
     int tiles_m, tiles_n, num_tiles;
-    int kb;                 // 64-deep K blocks of one product
-    int split_rows;         // DW: rows of a range, a multiple of 64
-    int which[3], num_which;  // DW: the gradients asked for
-    int first;              // DW: the slots start here
-    int wide_store;         // OUT, DX: 2 = 32-byte stores, 1 = 16-byte, 0 = single elements
+    int kb;           // 64-deep K blocks of one product
+    int tma_out;      // OUT, DX: rows of whole 16-byte units (else element by element)
+    // DW
+    int split_rows;   // rows of a range, a multiple of 64
+    int which[3], num_which;  // the gradients asked for
+    int tn01, tn2;    // column tiles of dWg and dWu, and of dWd
+    int tiles01, tiles2;      // tiles of one of dWg, dWu, and of dWd
+    int bn01;         // columns of a tile of dWg, dWu: 256 or 128
+    int direct;       // one range and one chunk: the tiles are the gradients
+    int first;        // the slots start here
 };
 
 template <int KIND, int BN, bool F16>
 struct TrCfg {
     static constexpr int THREADS = 384;
-    static constexpr int STAGES = 4;
+    static constexpr int STAGES = KIND == TR_GRAD ? 3 : 4;
+    static constexpr int BOXES = KIND == TR_GRAD ? 6144 : 4096;  // a warp's boxes for its results
     static constexpr int OPER_A = 128 * 128;   // 128 rows x 64 k, or 64 k x 128 columns
     static constexpr int OPER_B = BN * 128;
     static constexpr int STAGE_BYTES = OPER_A + OPER_B;
-    static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+    static constexpr int OFF_BOX = STAGES * STAGE_BYTES;
+    static constexpr int OFF_BAR = OFF_BOX + 8 * BOXES;
     static constexpr int BAR_FULL = 0, BAR_EMPTY = STAGES, BAR_AF = 2 * STAGES, BAR_AE = 2 * STAGES + 2,
                          BAR_DRAIN = 2 * STAGES + 4, NUM_BARS = 2 * STAGES + 5;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
@@ -161,32 +168,43 @@ __device__ __forceinline__ uint32_t tr_pack(float lo, float hi) {
     return F16 ? ptx::pack_f16x2(lo, hi) : ptx::pack_bf16x2(lo, hi);
 }
 
-// Eight words (16 elements) to 32-byte aligned global memory in one store.
-__device__ __forceinline__ void tr_st_global_x8(void* p, const uint32_t* w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+// 32 columns of this lane's row, packed, as 4 16-byte pieces `first` .. of a box
+// row: 32 rows of 64 bytes, 64 B swizzle.
+template <bool F16, int PIECES>
+__device__ __forceinline__ void tr_box16(uint32_t box, int lane, int first, const float* v) {
+#pragma unroll
+    for (int e = 0; e < PIECES; ++e)
+        ptx::st_shared_v4(box + swz_chunk<64>(lane, first + e),
+                          make_uint4(tr_pack<F16>(v[8 * e], v[8 * e + 1]), tr_pack<F16>(v[8 * e + 2], v[8 * e + 3]),
+                                     tr_pack<F16>(v[8 * e + 4], v[8 * e + 5]), tr_pack<F16>(v[8 * e + 6], v[8 * e + 7])));
 }
 
-// 32 columns c0 .. c0 + 31 of an output row of C columns.
+// 32 columns c0 .. of 32 rows m0 .. of an output whose rows TMA cannot store (no
+// whole 16-byte units): turned in a warp's 2 KB of shared memory, so that a store
+// covers 64 adjacent bytes of one row.  Word e of row r lies at r * 16 + (e ^ r % 16):
+// no bank is asked twice, either way.
 template <bool F16>
-__device__ __forceinline__ void tr_store_row(uint16_t* row, int c0, int C, int wide, const float* v) {
-    uint32_t w[16];
+__device__ __forceinline__ void tr_store_rows(uint32_t box, int lane, const float* v, uint16_t* out, int C, int c0, int m0,
+                                              int rows) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = tr_pack<F16>(v[2 * e], v[2 * e + 1]);
-    if (wide == 2) {
-        if (c0 < C) tr_st_global_x8(row + c0, w);
-        if (c0 + 16 < C) tr_st_global_x8(row + c0 + 16, w + 8);
-    } else if (wide == 1) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c0 + 8 * e < C)
-                *reinterpret_cast<uint4*>(row + c0 + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (c0 + e < C) row[c0 + e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+    for (int e = 0; e < 16; ++e)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(box + uint32_t(lane * 64 + ((e ^ (lane & 15)) << 2))),
+                     "r"(tr_pack<F16>(v[2 * e], v[2 * e + 1]))
+                     : "memory");
+    __syncwarp();
+    const int n = min(32, rows - m0);
+    if (c0 + lane < C) {
+        uint16_t* o = out + size_t(m0) * C + c0 + lane;
+#pragma unroll 8
+        for (int r = 0; r < n; ++r, o += C) {
+            uint16_t h;
+            asm volatile("ld.shared.u16 %0, [%1];"
+                         : "=h"(h)
+                         : "r"(box + uint32_t(r * 64 + (((lane >> 1) ^ (r & 15)) << 2) + 2 * (lane & 1))));
+            *o = h;
+        }
     }
+    __syncwarp();
 }
 
 template <int KIND, int ACT, bool F16, int BN>
@@ -205,18 +223,29 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
 
     // K blocks of one tile; GRAD runs dH's product first, then G and U; DX dG's, then dU's
     constexpr int PRODUCTS = (KIND == TR_GRAD || KIND == TR_DX) ? 2 : 1;
-    // tile L: column block fastest.  DW: gradient, then column and row block, then range of rows
+    // tile L: column block fastest, then row block.  DW: every tile of a range of
+    // rows (gradient by gradient), then the next range
     auto tile = [&](int L, int& tn, int& tm, int& which, int& split) {
         which = split = 0;
         if constexpr (KIND == TR_DW) {
-            which = p.which[L % p.num_which];
-            L /= p.num_which;
+            const int per = p.num_tiles;  // of a range
+            split = L / per;
+            L -= split * per;
+            for (int w = 0; w < p.num_which; ++w) {
+                which = p.which[w];
+                const int n = which == 2 ? p.tiles2 : p.tiles01;
+                if (L < n) break;
+                L -= n;
+            }
+            const int cols = which == 2 ? p.tn2 : p.tn01;
+            tn = L % cols;
+            tm = L / cols;
+        } else {
+            tn = L % p.tiles_n;
+            tm = L / p.tiles_n;
         }
-        tn = L % p.tiles_n;
-        L /= p.tiles_n;
-        tm = L % p.tiles_m;
-        split = L / p.tiles_m;
     };
+    const int all_tiles = KIND == TR_DW ? p.num_tiles * p.tiles_n : p.num_tiles;  // DW: tiles_n ranges
     auto blocks = [&](int split) -> int {
         if constexpr (KIND == TR_DW) {
             const int n = min(p.split_rows, p.rows - split * p.split_rows);
@@ -224,6 +253,7 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
         }
         return p.kb;
     };
+    auto dw_cols = [&](int which) -> int { return which == 2 ? 256 : p.bn01; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -251,7 +281,7 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
         // -------------------------------------------------------------- loads
         int n = 0;
         bool ok = true;
-        for (int L = blockIdx.x; L < p.num_tiles && ok; L += G) {
+        for (int L = blockIdx.x; L < all_tiles && ok; L += G) {
             int tn, tm, which, split;
             tile(L, tn, tm, which, split);
             const int kbs = blocks(split);
@@ -295,14 +325,13 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                         for (int x = 0; x < BN / 64; ++x)
                             ptx::tma_load_2d(b + 8192 * x, &maps.m[second ? 3 : 1], f, BN * tn + 64 * x, k);
                     } else {
-                        const int m = split * p.split_rows + k;
-                        ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
+                        const int m = split * p.split_rows + k, bn = dw_cols(which);
+                        ptx::mbar_arrive_expect_tx(f, uint32_t(C::OPER_A + bn * 128));
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            ptx::tma_load_2d(a + 8192 * x, &maps.m[which == 2 ? 1 : 0], f, 128 * tm + 64 * x, m);
-#pragma unroll
-                        for (int x = 0; x < BN / 64; ++x)
-                            ptx::tma_load_2d(b + 8192 * x, &maps.m[2 + which], f, BN * tn + 64 * x, m);
+                            ptx::tma_load_2d(a + 8192 * x, &maps.m[which == 2 ? 1 : 2 + which], f, 128 * tm + 64 * x, m);
+                        for (int x = 0; x < bn / 64; ++x)
+                            ptx::tma_load_2d(b + 8192 * x, &maps.m[which == 2 ? 4 : 0], f, bn * tn + 64 * x, m);
                     }
                 }
                 __syncwarp();
@@ -321,7 +350,7 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
         // --------------------------------------------------------------- MMAs
         int n = 0, t = 0;
         bool ok = true, issued = false;
-        for (int L = blockIdx.x; L < p.num_tiles && ok; L += G, ++t) {
+        for (int L = blockIdx.x; L < all_tiles && ok; L += G, ++t) {
             int tn, tm, which, split;
             tile(L, tn, tm, which, split);
             const int kbs = blocks(split), acc = t & 1;
@@ -357,8 +386,9 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                         constexpr bool A_MN = KIND == TR_DW, B_MN = KIND == TR_DW || KIND == TR_DX;
                         const uint64_t da = A_MN ? desc_mn_major<128>(a + 2048 * kk, 8192) : desc_k_major<128>(a + 32 * kk);
                         const uint64_t db = B_MN ? desc_mn_major<128>(b + 2048 * kk, 8192) : desc_k_major<128>(b + 32 * kk);
-                        ptx::mma_ss_elect(tmem + uint32_t(BN * acc), da, db, C::idesc(A_MN, B_MN, BN),
-                                          (kt > 0 || kk > 0) ? 1u : 0u);
+                        const uint32_t id = KIND == TR_DW && dw_cols(which) == 128 ? C::idesc(A_MN, B_MN, 128)
+                                                                                   : C::idesc(A_MN, B_MN, BN);
+                        ptx::mma_ss_elect(tmem + uint32_t(BN * acc), da, db, id, (kt > 0 || kk > 0) ? 1u : 0u);
                     }
                 }
                 issued = true;
@@ -375,14 +405,15 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
     } else if (warp >= 4) {
         // ----------------------------------------------------------- epilogue
         const int wq = warp & 3, half = (warp - 4) >> 2;
-        const int r = 32 * wq + lane;
         const uint32_t tl = tmem + (uint32_t(32 * wq) << 16);
+        const uint32_t box = sb + uint32_t(C::OFF_BOX + C::BOXES * (warp - 4));
         int t = 0;
+        uint32_t turn = 0;  // which of two boxes
         bool ok = true;
-        for (int L = blockIdx.x; L < p.num_tiles && ok; L += G, ++t) {
+        for (int L = blockIdx.x; L < all_tiles && ok; L += G, ++t) {
             int tn, tm, which, split;
             tile(L, tn, tm, which, split);
-            const int acc = t & 1;
+            const int acc = t & 1, m0 = 128 * tm + 32 * wq;
             ok = wait_warp(bar(C::BAR_AF + acc), uint32_t(t >> 1) & 1u, abort_flag);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -390,9 +421,20 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                 ptx::tc_fence_before();
                 ptx::mbar_arrive_elect(bar(C::BAR_AE + acc));
             };
+            // 32 columns c0 .. of this warp's rows of a 16-bit result through one of two boxes
+            auto put16 = [&](const CUtensorMap* map, int c0, int r0, const float* v) {
+                const uint32_t bx = box + 2048u * (turn & 1u);
+                ++turn;
+                ptx::bulk_wait_read<1>();  // the store before the last has read its box
+                __syncwarp();
+                tr_box16<F16, 4>(bx, lane, 0, v);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::tma_store_2d(map, bx, c0, r0);
+                __syncwarp();
+            };
             if constexpr (KIND == TR_GATE) {
                 // rows past `rows` and features past F are zero (their operands read as zero)
-                uint16_t* row = p.h + size_t(128 * tm + r) * p.ldf + 128 * tn + 64 * half;
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     float g[32], u[32];
@@ -401,18 +443,16 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
                     ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
                     if (c == 1) release();
-                    uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float2 h = tr_gate2<ACT>(make_float2(g[2 * e], g[2 * e + 1]),
                                                        make_float2(u[2 * e], u[2 * e + 1]));
-                        w[e] = tr_pack<F16>(h.x, h.y);
+                        g[2 * e] = h.x;
+                        g[2 * e + 1] = h.y;
                     }
-                    tr_st_global_x8(row + 32 * c, w);
-                    tr_st_global_x8(row + 32 * c + 16, w + 8);
+                    put16(&maps.m[3], 128 * tn + 64 * half + 32 * c, m0, g);
                 }
             } else if constexpr (KIND == TR_GRAD) {
-                const size_t at = size_t(128 * tm + r) * p.ldf + 128 * tn + 64 * half;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float g[16], u[16], d[16];
@@ -425,23 +465,35 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(d));
                     ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(d) + 8);
                     if (c == 3) release();
-                    uint32_t wh[8], wg[8], wu[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         float2 h, dg, du;
                         tr_grad2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]),
                                       make_float2(d[2 * e], d[2 * e + 1]), h, dg, du);
-                        wh[e] = tr_pack<F16>(h.x, h.y);
-                        wg[e] = tr_pack<F16>(dg.x, dg.y);
-                        wu[e] = tr_pack<F16>(du.x, du.y);
+                        d[2 * e] = h.x, d[2 * e + 1] = h.y;
+                        g[2 * e] = dg.x, g[2 * e + 1] = dg.y;
+                        u[2 * e] = du.x, u[2 * e + 1] = du.y;
                     }
-                    tr_st_global_x8(p.h + at + 16 * c, wh);
-                    tr_st_global_x8(p.dg + at + 16 * c, wg);
-                    tr_st_global_x8(p.du + at + 16 * c, wu);
+                    if ((c & 1) == 0) {  // the boxes of the 32 features before have been read
+                        ptx::bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+                    tr_box16<F16, 2>(box, lane, 2 * (c & 1), d);
+                    tr_box16<F16, 2>(box + 2048, lane, 2 * (c & 1), g);
+                    tr_box16<F16, 2>(box + 4096, lane, 2 * (c & 1), u);
+                    if (c & 1) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            const int c0 = 128 * tn + 64 * half + 32 * (c >> 1);
+#pragma unroll
+                            for (int o = 0; o < 3; ++o) ptx::tma_store_2d(&maps.m[5 + o], box + 2048u * o, c0, m0);
+                        }
+                        __syncwarp();
+                    }
                 }
             } else if constexpr (KIND == TR_DW) {
-                const int cols = BN / 2;
-                float* row = p.part + ((size_t(split) * 3 + which) * p.ldc + 128 * tm + r) * p.ldf2 + BN * tn + cols * half;
+                const int cols = dw_cols(which) / 2, R = which == 2 ? p.C : p.F, N = which == 2 ? p.F : p.C;
                 const bool empty = blocks(split) == 0;  // a range past the chunk's rows adds nothing
 #pragma unroll 1
                 for (int c = 0; c < cols / 32; ++c) {
@@ -449,21 +501,29 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     ptx::tmem_ld_x32(tl + uint32_t(BN * acc + cols * half + 32 * c), reinterpret_cast<uint32_t*>(v));
                     ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
                     if (c == cols / 32 - 1) release();
+                    const int c0 = dw_cols(which) * tn + cols * half + 32 * c;
+                    const bool in = c0 < N && m0 < R && !(empty && !p.first);
+                    if (in && p.direct) put16(&maps.m[5 + which], c0, m0, v);
+                    if (in && !p.direct) {
+                        ptx::bulk_wait_read<0>();
+                        __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float4* o = reinterpret_cast<float4*>(row + 32 * c + 4 * e);
-                        float4 x = empty ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                         : make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                        if (!p.first) {
-                            const float4 y = *o;
-                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        for (int e = 0; e < 8; ++e)
+                            ptx::st_shared_v4(box + swz_chunk<128>(lane, e),
+                                              empty ? make_uint4(0u, 0u, 0u, 0u)
+                                                    : make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                                                 __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3])));
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (p.first) ptx::tma_store_3d(&maps.m[5 + which], box, c0, m0, split);
+                            else ptx::tma_add_3d(&maps.m[5 + which], box, c0, m0, split);
                         }
-                        *o = x;
+                        __syncwarp();
                     }
                 }
             } else {
-                const int cols = BN / 2, m = 128 * tm + r;
-                uint16_t* row = p.out + size_t(m) * p.C;
+                const int cols = BN / 2;
 #pragma unroll 1
                 for (int c = 0; c < cols / 32; ++c) {
                     float v[32];
@@ -471,11 +531,15 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
                     if (c == cols / 32 - 1) release();
                     const int c0 = BN * tn + cols * half + 32 * c;
-                    if (m < p.rows) tr_store_row<F16>(row, c0, p.C, p.wide_store, v);
-                    __syncwarp();
+                    if (c0 < p.C && m0 < p.rows) {
+                        if (p.tma_out) put16(&maps.m[KIND == TR_OUT ? 2 : 4], c0, m0, v);
+                        else tr_store_rows<F16>(box, lane, v, p.out, p.C, c0, m0, p.rows);
+                    }
                 }
             }
         }
+        ptx::bulk_wait_all();  // the stores have left shared memory and are done
+        __syncwarp();
     }
 
     ptx::tc_fence_before();
@@ -757,7 +821,7 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
         auto drain = [&](int of_tile) -> bool {
             if (!wait_warp(bar(C::OF), uint32_t(t) & 1u, abort_flag)) return false;
             ptx::tc_fence_after();
-            const int m = 128 * of_tile + r;
+            const int m0 = 128 * of_tile + 32 * wq;
 #pragma unroll 1
             for (int c = 0; c < CN / 128; ++c) {
                 float v[32];
@@ -769,7 +833,7 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
                     ptx::mbar_arrive_elect(bar(C::OE));
                 }
                 if (p.wide_store) {
-                    ptx::bulk_wait_read();
+                    ptx::bulk_wait_read<0>();
                     __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -779,12 +843,10 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
                                                      tr_pack<F16>(v[8 * e + 6], v[8 * e + 7])));
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    const int m0 = 128 * of_tile + 32 * wq;
                     if (lane == 0 && m0 < p.M && c0 < p.C) ptx::tma_store_2d(&maps.m[4], ys, c0, m0);
                     __syncwarp();
                 } else {
-                    if (m < p.M) tr_store_row<F16>(p.out + size_t(m) * p.C, c0, p.C, 0, v);
-                    __syncwarp();
+                    if (m0 < p.M && c0 < p.C) tr_store_rows<F16>(ys, lane, v, p.out, p.C, c0, m0, p.M);
                 }
             }
             ++t;
@@ -842,45 +904,61 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
     if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// Rows of `w` elements copied to rows of `wp` (w rounded up to 8): TMA reads rows
-// of whole 16-byte units only.  What lies behind column w is never read.
-static __global__ void __launch_bounds__(256) evo_tr_pad_kernel(const uint16_t* __restrict__ x, uint16_t* __restrict__ y,
-                                                                long long rows, int w, int wp) {
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < rows * w; i += (long long)gridDim.x * blockDim.x) {
-        const long long r = i / w;
-        y[r * wp + (i - r * w)] = x[i];
+// Rows of `w` elements copied to rows of `wp` (w rounded up to 8), for up to five
+// matrices at once, a warp a row: TMA reads rows of whole 16-byte units only.
+// What lies behind column w is never read.
+struct TrPads {
+    const uint16_t* src[5];
+    uint16_t* dst[5];
+    int rows[5], w[5], wp[5];
+    int n;
+};
+
+static __global__ void __launch_bounds__(256) evo_tr_pad_kernel(const TrPads p) {
+    const int lane = threadIdx.x & 31;
+    int k = 0;
+    long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const long long step = ((long long)gridDim.x * blockDim.x) >> 5;
+    while (k < p.n) {
+        if (r >= p.rows[k]) {
+            r -= p.rows[k++];
+            continue;
+        }
+        const uint16_t* x = p.src[k] + r * p.w[k];
+        uint16_t* y = p.dst[k] + r * p.wp[k];
+#pragma unroll 4
+        for (int c = lane; c < p.w[k]; c += 32) y[c] = x[c];
+        r += step;
     }
 }
 
 // The weight gradients from their slots, added in order and rounded to the type:
-// slot 0 and 1 hold dWg and dWu as [C, F] and are written transposed, slot 2 holds dWd.
+// slots [splits][R][ld] of each gradient [R, N].
 template <typename T>
-__global__ void __launch_bounds__(256) evo_tr_mma_reduce_kernel(const float* __restrict__ part, int splits, int C, int F,
-                                                                int ldc, int ldf2, T* dwg, T* dwu, T* dwd) {
-    __shared__ float tile[32][33];
-    const int which = blockIdx.z;
-    T* out = which == 0 ? dwg : which == 1 ? dwu : dwd;
-    if (out == nullptr) return;
-    const int f0 = blockIdx.x * 32, c0 = blockIdx.y * 32, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const size_t slot = size_t(ldc) * ldf2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = c0 + ty + 8 * i, f = f0 + tx;  // inside the padded slot
-        float s = 0.0f;
-        for (int k = 0; k < splits; ++k) s += part[(size_t(k) * 3 + which) * slot + size_t(c) * ldf2 + f];
-        if (which == 2) {
-            if (c < C && f < F) tr_store(out + size_t(c) * F + f, s);
-        } else {
-            tile[ty + 8 * i][tx] = s;
-        }
+struct TrReduceParams {
+    const float* part[3];
+    T* out[3];
+    int R[3], N[3], ld[3];
+    int splits;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) evo_tr_mma_reduce_kernel(const TrReduceParams<T> p) {
+    const int w = blockIdx.z, n = (blockIdx.y * 64 + (threadIdx.x & 63)) * 4, r = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (p.out[w] == nullptr || r >= p.R[w] || n >= p.N[w]) return;
+    const size_t slot = size_t(p.R[w]) * p.ld[w];
+    const float* x = p.part[w] + size_t(r) * p.ld[w] + n;
+    float4 s = *reinterpret_cast<const float4*>(x);
+#pragma unroll 4
+    for (int k = 1; k < p.splits; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(x + k * slot);
+        s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
     }
-    if (which == 2) return;
-    __syncthreads();
+    T* o = p.out[w] + size_t(r) * p.N[w] + n;
+    const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int f = f0 + ty + 8 * i, c = c0 + tx;
-        if (c < C && f < F) tr_store(out + size_t(f) * C + c, tile[tx][ty + 8 * i]);
-    }
+    for (int e = 0; e < 4; ++e)
+        if (n + e < p.N[w]) tr_store(o + e, v[e]);
 }
 
 }  // namespace evo
