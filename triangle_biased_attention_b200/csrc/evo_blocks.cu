@@ -429,42 +429,6 @@ bool encode_slots(CUtensorMap* m, void* base, int64_t splits, int64_t R, int64_t
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// H, dG, dU and dX of one chunk in one kernel (C <= 128), with the maps of GRAD and DX.
-template <int ACT, bool F16>
-int launch_gradx(int dev, int sms, const evo::TrMaps& grad, const evo::TrMaps& dx, uint16_t* out, void* dg, void* du, int rows,
-                 int64_t C, int64_t F, cudaStream_t st) {
-    using Cfg = evo::TrGradxCfg<F16>;
-    auto kernel = evo::evo_tr_gradx_kernel<ACT, F16>;
-    static AttrOnce attr;
-    if (!attr.ensure(dev, kernel, Cfg::SMEM_BYTES)) return EVO_ERR_CUDA;
-    evo::TrGradxParams p = {};
-    p.out = out;
-    p.M = rows;
-    p.C = int(C);
-    p.F = int(F);
-    p.num_tiles = tiles_of(rows, 128);
-    p.kc = tiles_of(C, 64);
-    p.chunks = tiles_of(F, 128);
-    p.tma_out = out && tma_rows(out, C);
-    const int64_t ldf = round_up(F, 128);
-    evo::TrMaps a = grad, b;  // X, dY, Wg, Wu, Wd, H, dG, dU
-    a.m[1] = grad.m[3];
-    a.m[2] = grad.m[1];
-    a.m[3] = grad.m[2];
-    std::memset(&b, 0, sizeof(b));
-    b.m[0] = dx.m[1];
-    b.m[1] = dx.m[3];
-    if (!encode_rows(&a.m[6], dg, rows, ldf, ldf, 32, F16) || !encode_rows(&a.m[7], du, rows, ldf, ldf, 32, F16) ||
-        (p.tma_out && !encode_rows(&b.m[2], out, rows, C, C, 32, F16, 32)))
-        return EVO_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min(p.num_tiles, sms)), 1, 1);
-    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
-    cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, kernel, a, b, p) == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
-}
-
 template <bool F16, int ACT>
 int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const void* Wd, const void* dY, void* dX,
                 void* dWg, void* dWu, void* dWd, char* ws, int64_t M, int64_t C, int64_t F, int dtype, cudaStream_t st) {
@@ -523,13 +487,8 @@ int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
         p.tiles_n = tiles_of(F, 128);
         p.num_tiles = p.tiles_m * p.tiles_n;
         p.kb = tiles_of(C, 64);
-        if (C <= 128 && p.rows > 64 * 128) {
-            if (launch_gradx<ACT, F16>(dev, sms, grad, out, dX ? static_cast<uint16_t*>(dX) + m * C : nullptr, dg, du, p.rows, C,
-                                       F, st) != EVO_OK)
-                return EVO_ERR_CUDA;
-        } else if (launch_mma<evo::TR_GRAD, ACT, F16, 256>(dev, sms, grad, p, st) != EVO_OK) {
-            return EVO_ERR_CUDA;
-        } else if (dX && launch_out<evo::TR_DX, F16>(dev, sms, out, p, static_cast<uint16_t*>(dX) + m * C, st) != EVO_OK)
+        if (launch_mma<evo::TR_GRAD, ACT, F16, 256>(dev, sms, grad, p, st) != EVO_OK) return EVO_ERR_CUDA;
+        if (dX && launch_out<evo::TR_DX, F16>(dev, sms, out, p, static_cast<uint16_t*>(dX) + m * C, st) != EVO_OK)
             return EVO_ERR_CUDA;
         if (p.num_which > 0) {
             p.num_tiles = dw_tiles;

@@ -904,363 +904,6 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
     if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// ------------------------------------------------ H, dG, dU and dX in one kernel
-
-// For C <= 128 the backward's row products run in one kernel: dG and dU, which
-// have to leave for the weight gradients anyway, lie in shared memory as the
-// tensor core reads them, and dX = dG Wg + dU Wu accumulates in 128 columns of
-// tensor memory.  Apart, GRAD and DX were both bound by memory (147456 rows x 512
-// features: 112 and 55 us); here dG and dU are not read back.  What bounds it is
-// the three [rows, F] arrays written, 96 KB for 128 rows x 128 features.
-//
-// Per chunk of 128 features: G, U and dH in 384 columns of tensor memory, X and
-// dY of the 128 rows stay in shared memory; eight warps turn them into tiles of
-// dG and dU and boxes of H.  Warp 1 issues G, U and dH, warp 2 dX, each from a
-// ring of 16 KB weight stages of its own (loaded by warps 0 and 3): GU(q + 1) runs
-// beside the activation of chunk q, dX of chunk q beside that of chunk q + 1.
-struct TrGradxParams {
-    uint16_t* out;  // dX [M, C], or null
-    int M, C, F;
-    int num_tiles;  // ceil(M / 128)
-    int kc;         // 64-deep blocks of C: 1 or 2
-    int chunks;     // ceil(F / 128)
-    int tma_out;    // dX through TMA
-};
-
-template <bool F16>
-struct TrGradxCfg {
-    static constexpr int EPI_WARPS = 8;
-    static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-    static constexpr int XSLOTS = 4;               // 128 rows x 64 k of X or dY
-    static constexpr int ASTAGES = 3, BSTAGES = 2;  // 16 KB weight stages: G, U, dH and dX
-    static constexpr int OFF_D = XSLOTS * 16384;   // dG, dU: 128 rows x 128 features each, 64 columns a sub-tile
-    static constexpr int OFF_BOX = OFF_D + 65536;  // 2 KB a warp: 32 rows x 32 columns of H or dX
-    static constexpr int OFF_A = OFF_BOX + EPI_WARPS * 2048;
-    static constexpr int OFF_B = OFF_A + ASTAGES * 16384;
-    static constexpr int OFF_BAR = OFF_B + BSTAGES * 16384;
-    static constexpr int XF = 0, XE = XF + XSLOTS, AF = XE + XSLOTS, AE = AF + ASTAGES, BF = AE + ASTAGES, BE = BF + BSTAGES,
-                         GF = BE + BSTAGES, GE = GF + 1, DF = GE + 1, DE = DF + 1, OF = DE + 1, OE = OF + 1, DRAIN = OE + 1,
-                         NUM_BARS = DRAIN + 2;
-    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-    static constexpr uint32_t TMEM_COLS = 512;     // G 0, U 128, dH 256, dX 384
-    static constexpr uint32_t AB = F16 ? 0u : ((1u << 7) | (1u << 10));
-    __host__ __device__ static constexpr uint32_t idesc(bool b_mn) {  // M = N = 128
-        return (1u << 4) | AB | (b_mn ? 1u << 16 : 0u) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-    }
-};
-
-// maps: X, dY (boxes of 128 rows), Wg, Wu (128 rows), Wd (64 rows), H (32 x 32), dG,
-// dU (64 columns x 32 rows); maps2: Wg, Wu (64 rows), dX (32 x 32)
-template <int ACT, bool F16>
-__global__ void __launch_bounds__(384, 1)
-evo_tr_gradx_kernel(const __grid_constant__ TrMaps maps, const __grid_constant__ TrMaps maps2, const TrGradxParams p) {
-    using C = TrGradxCfg<F16>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sb = ptx::smem_u32(smem);
-    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
-    const int lane = threadIdx.x & 31;
-    const int G = gridDim.x;
-    auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8u * uint32_t(i); };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-    const int my_tiles = (p.num_tiles - int(blockIdx.x) + G - 1) / G;
-    const int total = my_tiles * p.chunks;  // this CTA's chunks, in order
-    const bool need_dx = p.out != nullptr;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NUM_BARS; ++i)
-            ptx::mbar_init(bar(i), i == C::GE || i == C::DF || i == C::OE ? C::EPI_WARPS : 1);
-        *abort_flag = 0;
-        ptx::fence_mbar_init();
-    }
-    if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
-        ptx::tmem_relinquish();
-    }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-
-    if (warp == 0) {
-        // ------------------------------------- loads: X, dY and the weights of G, U, dH
-        int n = 0, xn = 0;
-        bool ok = true;
-        int tile = blockIdx.x, j = 0;
-        for (int q = 0; q < total && ok; ++q) {
-            if (j == 0) {
-                for (int k = 0; k < 2 * p.kc && ok; ++k, ++xn) {  // X's blocks, then dY's
-                    const int s = xn % C::XSLOTS;
-                    ok = wait_warp(bar(C::XE + s), ((xn / C::XSLOTS) & 1) ^ 1, abort_flag);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        const bool dy = k >= p.kc;
-                        ptx::mbar_arrive_expect_tx(bar(C::XF + s), 16384);
-                        ptx::tma_load_2d(sb + uint32_t(16384 * s), &maps.m[dy ? 1 : 0], bar(C::XF + s), 64 * (dy ? k - p.kc : k),
-                                         128 * tile);
-                    }
-                    __syncwarp();
-                }
-            }
-            for (int st = 0; st < 3 * p.kc && ok; ++st, ++n) {  // Wg, Wu of each block, then Wd's blocks
-                const int s = n % C::ASTAGES;
-                ok = wait_warp(bar(C::AE + s), ((n / C::ASTAGES) & 1) ^ 1, abort_flag);
-                if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t d = sb + uint32_t(C::OFF_A + 16384 * s), f = bar(C::AF + s);
-                    ptx::mbar_arrive_expect_tx(f, 16384);
-                    if (st < 2 * p.kc) {
-                        ptx::tma_load_2d(d, &maps.m[st & 1 ? 3 : 2], f, 64 * (st >> 1), 128 * j);
-                    } else {
-                        const int k = 64 * (st - 2 * p.kc);
-                        ptx::tma_load_2d(d, &maps.m[4], f, 128 * j, k);
-                        ptx::tma_load_2d(d + 8192, &maps.m[4], f, 128 * j + 64, k);
-                    }
-                }
-                __syncwarp();
-            }
-            if (++j == p.chunks) {
-                j = 0;
-                tile += G;
-            }
-        }
-        if (!ok && lane == 0) {
-            // the last load of each slot and stage lands before the CTA exits
-            for (int s = 0; s < C::ASTAGES; ++s)
-                if (n - 1 >= s) wait_bounded(bar(C::AF + s), uint32_t((n - 1 - s) / C::ASTAGES) & 1u, nullptr);
-            for (int s = 0; s < C::XSLOTS; ++s)
-                if (xn - 1 >= s) wait_bounded(bar(C::XF + s), uint32_t((xn - 1 - s) / C::XSLOTS) & 1u, nullptr);
-        }
-        __syncwarp();
-    } else if (warp == 3) {
-        // ----------------------------------------------- loads: the weights of dX
-        int n = 0;
-        bool ok = true;
-        int j = 0;
-        for (int q = 0; q < total && ok && need_dx; ++q) {
-            for (int st = 0; st < 4 && ok; ++st, ++n) {  // 64 features x 128 channels of Wg (twice), then of Wu
-                const int s = n % C::BSTAGES;
-                ok = wait_warp(bar(C::BE + s), ((n / C::BSTAGES) & 1) ^ 1, abort_flag);
-                if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t d = sb + uint32_t(C::OFF_B + 16384 * s), f = bar(C::BF + s);
-                    const int f0 = 128 * j + 64 * (st & 1);
-                    ptx::mbar_arrive_expect_tx(f, 16384);
-                    ptx::tma_load_2d(d, &maps2.m[st >> 1], f, 0, f0);
-                    ptx::tma_load_2d(d + 8192, &maps2.m[st >> 1], f, 64, f0);
-                }
-                __syncwarp();
-            }
-            if (++j == p.chunks) j = 0;
-        }
-        if (!ok && lane == 0)
-            for (int s = 0; s < C::BSTAGES; ++s)
-                if (n - 1 >= s) wait_bounded(bar(C::BF + s), uint32_t((n - 1 - s) / C::BSTAGES) & 1u, nullptr);
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------- G, U, dH products
-        int n = 0, xn = 0, j = 0;
-        bool ok = true, issued = false;
-        for (int q = 0; q < total && ok; ++q) {
-            ok = wait_warp(bar(C::GE), (q & 1) ^ 1, abort_flag);  // the chunk before has been read
-            if (!ok) break;
-            ptx::tc_fence_after();
-            for (int st = 0; st < 3 * p.kc; ++st, ++n) {
-                const int s = n % C::ASTAGES, dh = st >= 2 * p.kc;
-                const int k = dh ? st - p.kc : st >> 1;  // slot of the tile: X's blocks, then dY's
-                const int x = (xn + k) % C::XSLOTS;
-                if (j == 0 && (dh || !(st & 1))) {
-                    ok = wait_warp(bar(C::XF + x), uint32_t((xn + k) / C::XSLOTS) & 1u, abort_flag);
-                    if (!ok) break;
-                }
-                ok = wait_warp(bar(C::AF + s), uint32_t(n / C::ASTAGES) & 1u, abort_flag);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t a = sb + uint32_t(16384 * x), b = sb + uint32_t(C::OFF_A + 16384 * s);
-                const uint32_t d = tmem + (dh ? 256u : 128u * uint32_t(st & 1));
-                const uint32_t first = (dh ? st == 2 * p.kc : st < 2) ? 0u : 1u;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint64_t db = dh ? desc_mn_major<128>(b + 2048 * kk, 8192) : desc_k_major<128>(b + 32 * kk);
-                    ptx::mma_ss_elect(d, desc_k_major<128>(a + 32 * kk), db, C::idesc(dh), kk > 0 ? 1u : first);
-                }
-                issued = true;
-                ptx::mma_commit_elect(bar(C::AE + s));
-                if (j == p.chunks - 1 && (dh || (st & 1))) ptx::mma_commit_elect(bar(C::XE + x));
-            }
-            if (!ok) break;
-            ptx::mma_commit_elect(bar(C::GF));
-            if (++j == p.chunks) {
-                j = 0;
-                xn += 2 * p.kc;
-            }
-        }
-        if (!ok && issued) {
-            ptx::mma_commit_elect(bar(C::DRAIN));
-            wait_bounded(bar(C::DRAIN), 0, nullptr);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ dX products
-        int n = 0, j = 0, t = 0;
-        bool ok = true, issued = false;
-        for (int q = 0; q < total && ok && need_dx; ++q) {
-            if (j == 0) {  // the tile before has been drained
-                ok = wait_warp(bar(C::OE), (t & 1) ^ 1, abort_flag);
-                if (!ok) break;
-            }
-            ok = wait_warp(bar(C::DF), uint32_t(q) & 1u, abort_flag);
-            if (!ok) break;
-            for (int st = 0; st < 4; ++st, ++n) {
-                const int s = n % C::BSTAGES;
-                ok = wait_warp(bar(C::BF + s), uint32_t(n / C::BSTAGES) & 1u, abort_flag);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t a = sb + uint32_t(C::OFF_D + 16384 * st), b = sb + uint32_t(C::OFF_B + 16384 * s);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    ptx::mma_ss_elect(tmem + 384u, desc_k_major<128>(a + 32 * kk), desc_mn_major<128>(b + 2048 * kk, 8192),
-                                      C::idesc(true), (j > 0 || st > 0 || kk > 0) ? 1u : 0u);
-                issued = true;
-                ptx::mma_commit_elect(bar(C::BE + s));
-            }
-            if (!ok) break;
-            ptx::mma_commit_elect(bar(C::DE));
-            if (++j == p.chunks) {
-                ptx::mma_commit_elect(bar(C::OF));
-                j = 0;
-                ++t;
-            }
-        }
-        if (!ok && issued) {
-            ptx::mma_commit_elect(bar(C::DRAIN + 1));
-            wait_bounded(bar(C::DRAIN + 1), 0, nullptr);
-        }
-        __syncwarp();
-    } else {
-        // ---------------------------------------------------------- activations
-        const int wq = warp & 3, half = (warp - 4) >> 2;
-        const int r = 32 * wq + lane;
-        const uint32_t tl = tmem + (uint32_t(32 * wq) << 16);
-        const uint32_t box = sb + uint32_t(C::OFF_BOX + 2048 * (warp - 4));
-        const uint32_t dg = sb + uint32_t(C::OFF_D + 16384 * half), du = dg + 32768u;
-        bool ok = true;
-        int t = 0;  // tiles drained
-        auto drain = [&]() -> bool {
-            if (!wait_warp(bar(C::OF), uint32_t(t) & 1u, abort_flag)) return false;
-            ptx::tc_fence_after();
-            const int m0 = 128 * (int(blockIdx.x) + t * G) + 32 * wq;
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                float v[32];
-                const int c0 = 64 * half + 32 * c;
-                ptx::tmem_ld_x32(tl + uint32_t(384 + c0), reinterpret_cast<uint32_t*>(v));
-                ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
-                if (c == 1) {
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive_elect(bar(C::OE));
-                }
-                if (c0 < p.C && m0 < p.M) {
-                    ptx::bulk_wait_read<0>();
-                    __syncwarp();
-                    if (p.tma_out) {
-                        tr_box16<F16, 4>(box, lane, 0, v);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) ptx::tma_store_2d(&maps2.m[2], box, c0, m0);
-                        __syncwarp();
-                    } else {
-                        tr_store_rows<F16>(box, lane, v, p.out, p.C, c0, m0, p.M);
-                    }
-                }
-            }
-            ++t;
-            return true;
-        };
-        int tile = blockIdx.x, j = 0;
-        for (int q = 0; q < total && ok; ++q) {
-            ok = wait_warp(bar(C::GF), uint32_t(q) & 1u, abort_flag);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const int m0 = 128 * tile + 32 * wq, f0 = 128 * j + 64 * half;
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                float g[32], u[32], d[32];
-                ptx::tmem_ld_x32(tl + uint32_t(64 * half + 32 * c), reinterpret_cast<uint32_t*>(g));
-                ptx::tmem_ld_x32(tl + uint32_t(128 + 64 * half + 32 * c), reinterpret_cast<uint32_t*>(u));
-                ptx::tmem_ld_x32(tl + uint32_t(256 + 64 * half + 32 * c), reinterpret_cast<uint32_t*>(d));
-                ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
-                ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
-                ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(d));
-                if (c == 1) {
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive_elect(bar(C::GE));
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 hv, dgv, duv;
-                    tr_grad2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]),
-                                  make_float2(d[2 * e], d[2 * e + 1]), hv, dgv, duv);
-                    d[2 * e] = hv.x, d[2 * e + 1] = hv.y;
-                    g[2 * e] = dgv.x, g[2 * e + 1] = dgv.y;
-                    u[2 * e] = duv.x, u[2 * e + 1] = duv.y;
-                }
-                if (c == 0 && need_dx) {  // the product of the chunk before has read dG and dU
-                    ok = wait_warp(bar(C::DE), uint32_t(q & 1) ^ 1u, abort_flag);
-                    if (!ok) break;
-                }
-                if (c == 0) {  // and so have this warp's stores
-                    ptx::bulk_wait_read<0>();
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t at = swz_chunk<128>(r, 4 * c + e);
-                    ptx::st_shared_v4(dg + at, make_uint4(tr_pack<F16>(g[8 * e], g[8 * e + 1]), tr_pack<F16>(g[8 * e + 2], g[8 * e + 3]),
-                                                          tr_pack<F16>(g[8 * e + 4], g[8 * e + 5]),
-                                                          tr_pack<F16>(g[8 * e + 6], g[8 * e + 7])));
-                    ptx::st_shared_v4(du + at, make_uint4(tr_pack<F16>(u[8 * e], u[8 * e + 1]), tr_pack<F16>(u[8 * e + 2], u[8 * e + 3]),
-                                                          tr_pack<F16>(u[8 * e + 4], u[8 * e + 5]),
-                                                          tr_pack<F16>(u[8 * e + 6], u[8 * e + 7])));
-                }
-                if (c == 1) {  // the box of the first half
-                    ptx::bulk_wait_read<0>();
-                    __syncwarp();
-                }
-                tr_box16<F16, 4>(box, lane, 0, d);
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::tma_store_2d(&maps.m[5], box, f0 + 32 * c, m0);
-                    if (c == 1) {  // both halves of the 64 features: one box each
-                        ptx::tma_store_2d(&maps.m[6], dg + uint32_t(4096 * wq), f0, m0);
-                        ptx::tma_store_2d(&maps.m[7], du + uint32_t(4096 * wq), f0, m0);
-                    }
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
-            ptx::mbar_arrive_elect(bar(C::DF));
-            if (need_dx && j == 0 && q > 0) ok = drain();
-            if (++j == p.chunks) {
-                j = 0;
-                tile += G;
-            }
-        }
-        if (need_dx && ok && total > 0) drain();
-        ptx::bulk_wait_all();  // the stores have left shared memory and are done
-        __syncwarp();
-    }
-
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
-}
-
 // Rows of `w` elements copied to rows of `wp` (w rounded up to 8), for up to five
 // matrices at once, a warp a row: TMA reads rows of whole 16-byte units only.
 // What lies behind column w is never read.
