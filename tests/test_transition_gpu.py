@@ -100,6 +100,28 @@ def test_msa_size(C, F):
     assert evo.evo_attn_sync_status() == evo.EVO_OK
 
 
+@pytest.mark.parametrize("shape,dt", [((8321, 128, 512), BF16), ((8200, 40, 72), FP16), ((20001, 64, 264), BF16),
+                                      ((8193, 100, 130), BF16), ((38000, 128, 128), FP16), ((8193, 1, 1), BF16),
+                                      ((60000, 128, 300), BF16), ((20000, 200, 264), BF16)], ids=str)
+def test_backward_many_rows_of_few_channels(shape, dt):
+    """Long row counts over narrow blocks: ragged tiles in every direction, all
+    gradients and each side alone."""
+    M, C, F = shape
+    act = "gelu" if M % 2 else "silu"
+    x, wg, wu, wd, dy = make(M, C, F, dt, seed=M)
+    grads = evo.transition_backward(x, wg, wu, wd, dy, act=act)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    ref, err = T.backward(x, wg, wu, wd, dy, act, dt)
+    for name, g, r, e in zip(("dx", "dw_gate", "dw_up", "dw_down"), grads, ref, err):
+        within(g, r, e, f"{shape} {dt} {name}")
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(evo.transition_backward(x, wg, wu, wd, dy, act=act), grads))
+    assert torch.equal(evo.transition_backward(x, wg, wu, wd, dy, act=act, need_dw=False)[0], grads[0])
+    none, *dw = evo.transition_backward(x, wg, wu, wd, dy, act=act, need_dx=False)
+    assert none is None and all(torch.equal(a, b) for a, b in zip(dw, grads[1:]))
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+
+
 def test_activation_range():
     """Gates far out on both sides: no overflow on the way to 0 or to g."""
     gates = torch.tensor([-1e30, -3e4, -100.0, -88.5, -87.0, -20.0, -1.0, -0.0, 1e-30, 20.0, 100.0, 1e3])
