@@ -470,10 +470,14 @@ class _OnStream:
     def __init__(self, stream: Optional[torch.cuda.Stream], device):
         if device.type != "cuda":
             raise ValueError("tensors must be on a CUDA device")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.scope = None if stream is None else torch.cuda.stream(stream)
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        if stream is None:
+            self.scope = None
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.scope = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
 
     def __enter__(self):
         if self.scope is not None:

@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "host_util.cuh"
 #include "relpos.cuh"
+#include "transition_few.cuh"
 #include "transition_simt.cuh"
 #include "transition_sm100.cuh"
 
@@ -89,11 +90,17 @@ struct TrLayout {
     int64_t part = 0, part2 = 0, part3 = 0;       // partial weight gradients, fp32: [splits][R][N up to 4] (fp32 call: one)
     bool direct = false;                          // 16-bit: the last products are the weight gradients
     int64_t splits = 0, split_rows = 0;           // ranges of rows with a slot of their own
+    bool few = false;                             // the forward's form for a few rows: H [M, F] in fp32
     bool fused = false;                           // the forward's one-kernel form: no [M, F] array at all
     int64_t x = 0, dy = 0, wg = 0, wu = 0, wd = 0;  // 16-bit, odd C or F: copies with rows of whole 16-byte units
     bool pad = false;
     int64_t total = 0;
 };
+
+// The form for a few rows reads X and H from shared memory.
+bool tr_few(int64_t M, int64_t C, int64_t F) {
+    return M <= evo::kTrFewRows && 8 * C * 4 <= evo::kTrFewBytes && 8 * F * 4 <= evo::kTrFewBytes;
+}
 
 // The one-kernel forward holds Y of 128 rows in tensor memory (C <= 256) and
 // gives a tile of rows to one SM, so it wants tiles for most of them.
@@ -104,6 +111,12 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
     const int64_t es = elem_bytes(dtype);
     // C, F <= 2^20 and M < 2^31 (check_transition): the products below fit
     const int64_t fc = F * C;
+    if (!backward && tr_few(M, C, F)) {
+        L->few = true;
+        L->chunk = M;
+        L->total = round_up(M * F * 4, 256);
+        return true;
+    }
     const int64_t ldf = dtype == EVO_DTYPE_FP32 ? F : round_up(F, 128);
     L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
     L->fused = !backward && tr_fused(M, C, dtype);
@@ -164,14 +177,33 @@ int check_transition(int64_t M, int64_t C, int64_t F, int act, int dtype) {
 
 constexpr int kTrSmem = 4 * evo::kTrK * evo::kTrLd * int(sizeof(float));
 
-template <typename K, typename P>
-bool launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const P& p) {
+// Launches a kernel; `dependent`: it may start while the kernel before it in the
+// stream still runs (it waits for that one's end itself).
+template <typename K, typename... P>
+bool launch_any(bool dependent, K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const P&... p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    if (dependent) {
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, p...) == cudaSuccess;
+}
+
+template <typename K, typename P>
+bool launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const P& p) {
+    return launch_any(false, kernel, grid, threads, smem, st, p);
+}
+
+template <typename K, typename... P>
+bool launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const P&... p) {
+    return launch_any(true, kernel, grid, threads, smem, st, p...);
 }
 
 unsigned blocks_of(int64_t n, int64_t tile) { return unsigned((n + tile - 1) / tile); }
@@ -269,13 +301,10 @@ int launch_mma(int dev, int sms, const evo::TrMaps& maps, const evo::TrMmaParams
     auto kernel = evo::evo_tr_mma_kernel<KIND, ACT, F16, BN>;
     static AttrOnce attr;
     if (!attr.ensure(dev, kernel, Cfg::SMEM_BYTES)) return EVO_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
     const int tiles = KIND == evo::TR_DW ? p.num_tiles * p.tiles_n : p.num_tiles;
-    cfg.gridDim = dim3(unsigned(std::min(tiles, sms)), 1, 1);
-    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
-    cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, p) == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+    return launch_dependent(kernel, dim3(unsigned(std::min(tiles, sms))), Cfg::THREADS, Cfg::SMEM_BYTES, st, maps, p)
+               ? EVO_OK
+               : EVO_ERR_CUDA;
 }
 
 // What a 16-bit call reads through TMA: the tensors themselves, or copies with
@@ -297,7 +326,7 @@ struct PadList {
     bool run(int sms, cudaStream_t st) {
         int64_t rows = 0;
         for (int k = 0; k < p.n; ++k) rows += p.rows[k];
-        return launch(evo::evo_tr_pad_kernel, dim3(unsigned(std::min<int64_t>((rows + 7) / 8, int64_t(sms) * 8))), 256, 0, st, p);
+        return launch_dependent(evo::evo_tr_pad_kernel, dim3(unsigned(std::min<int64_t>((rows + 7) / 8, int64_t(sms) * 8))), 256, 0, st, p);
     }
 };
 
@@ -366,12 +395,9 @@ int launch_fused(int dev, int sms, const void* x, const TrSource& s, uint16_t* y
     p.kc = tiles_of(C, 64);
     p.chunks = tiles_of(F, 128);
     p.wide_store = wide;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min(p.num_tiles, sms)), 1, 1);
-    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
-    cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, p) == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+    return launch_dependent(kernel, dim3(unsigned(std::min(p.num_tiles, sms))), Cfg::THREADS, Cfg::SMEM_BYTES, st, maps, p)
+               ? EVO_OK
+               : EVO_ERR_CUDA;
 }
 
 template <bool F16, int ACT>
@@ -507,10 +533,50 @@ int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
             r.ld[w] = int(round_up(r.N[w], 4));
         }
         const int64_t big = std::max(C, F);
-        if (!launch(evo::evo_tr_mma_reduce_kernel<T>, dim3(blocks_of(big, 4), blocks_of(big, 256), 3), 256, 0, st, r))
+        if (!launch_dependent(evo::evo_tr_mma_reduce_kernel<T>, dim3(blocks_of(big, 4), blocks_of(big, 256), 3), 256, 0, st, r))
             return EVO_ERR_CUDA;
     }
     return EVO_OK;
+}
+
+template <typename T, int ACT, int MB>
+int run_few(int dev, const evo::TrFewParams<T>& p, bool vec, cudaStream_t st) {
+    constexpr int VE = 16 / int(sizeof(T));
+    auto gate = vec ? evo::evo_tr_few_gate_kernel<T, ACT, MB, VE> : evo::evo_tr_few_gate_kernel<T, ACT, MB, 1>;
+    auto out = vec ? evo::evo_tr_few_out_kernel<T, MB, VE> : evo::evo_tr_few_out_kernel<T, MB, 1>;
+    static AttrOnce attr[2][2];
+    if (!attr[0][vec].ensure(dev, gate, evo::kTrFewBytes) || !attr[1][vec].ensure(dev, out, evo::kTrFewBytes))
+        return EVO_ERR_CUDA;
+    const unsigned blocks = std::min(blocks_of(p.F, 8), 148u * 8);
+    const unsigned channels = blocks_of(p.C, 8 / p.split);
+    return launch_dependent(gate, dim3(blocks), evo::kTrFewThreads, MB * p.C * 4, st, p) &&
+                   launch_dependent(out, dim3(channels), evo::kTrFewThreads, MB * p.F * 4, st, p)
+               ? EVO_OK
+               : EVO_ERR_CUDA;
+}
+
+template <typename T>
+int run_fwd_few(int dev, const void* X, const void* Wg, const void* Wu, const void* Wd, void* Y, char* ws, int64_t M, int64_t C,
+                int64_t F, int act, cudaStream_t st) {
+    constexpr int VE = 16 / int(sizeof(T));
+    evo::TrFewParams<T> p = {};
+    p.x = static_cast<const T*>(X);
+    p.wg = static_cast<const T*>(Wg);
+    p.wu = static_cast<const T*>(Wu);
+    p.wd = static_cast<const T*>(Wd);
+    p.y = static_cast<T*>(Y);
+    p.h = reinterpret_cast<float*>(ws);
+    p.M = int(M);
+    p.C = int(C);
+    p.F = int(F);
+    // warps enough for every SM, while each still reads whole rounds of its row
+    p.split = 1;
+    while (p.split < 8 && C * p.split < 148 * 8 && F >= int64_t(2) * p.split * 32 * VE) p.split *= 2;
+    const bool vec = C % VE == 0 && F % VE == 0 && aligned(Wg, 16) && aligned(Wu, 16) && aligned(Wd, 16);
+    const bool silu = act == EVO_ACT_SILU;
+    if (M == 1) return silu ? run_few<T, EVO_ACT_SILU, 1>(dev, p, vec, st) : run_few<T, EVO_ACT_GELU, 1>(dev, p, vec, st);
+    if (M <= 4) return silu ? run_few<T, EVO_ACT_SILU, 4>(dev, p, vec, st) : run_few<T, EVO_ACT_GELU, 4>(dev, p, vec, st);
+    return silu ? run_few<T, EVO_ACT_SILU, 8>(dev, p, vec, st) : run_few<T, EVO_ACT_GELU, 8>(dev, p, vec, st);
 }
 
 int64_t tr_workspace(int64_t M, int64_t C, int64_t F, int dtype, bool backward) {
@@ -574,6 +640,10 @@ extern "C" EVO_API int evo_transition_fwd(const void* X, const void* Wg, const v
     const int dev = select_device({X, Wg, Wu, Wd, Y, workspace}, scope);
     if (dev < 0) return dev;
     char* ws = static_cast<char*>(workspace);
+    if (L.few) {
+        auto run = dtype == EVO_DTYPE_FP32 ? run_fwd_few<float> : dtype == EVO_DTYPE_FP16 ? run_fwd_few<__half> : run_fwd_few<__nv_bfloat16>;
+        return run(dev, X, Wg, Wu, Wd, Y, ws, M, C, F, act, st);
+    }
     if (dtype == EVO_DTYPE_FP32) {
         auto f = [](const void* p) { return static_cast<const float*>(p); };
         auto run = act == EVO_ACT_SILU ? run_fwd_simt<EVO_ACT_SILU> : run_fwd_simt<EVO_ACT_GELU>;

@@ -339,6 +339,13 @@ __device__ __forceinline__ void setmaxnreg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Programmatic dependent launch: a kernel launched with the attribute may start
+// while the kernel before it in the stream still runs; it waits for that kernel's
+// end (and its memory) before it touches anything the other may read or write.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next such kernel be scheduled as soon as this one leaves it room.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // -------------------------------------------------------------- scalar ops
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;

@@ -276,6 +276,8 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    ptx::pdl_launch();
+    ptx::pdl_wait();
 
     if (warp == 0) {
         // -------------------------------------------------------------- loads
@@ -648,6 +650,8 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    ptx::pdl_launch();
+    ptx::pdl_wait();
     // Fill n of the weight ring has landed.  Two warps take stages from the one
     // ring.  A parity cannot tell fill n of a stage from the one two fills before,
     // so a warp must know that the fill between, which may be the other warp's, has
@@ -915,6 +919,8 @@ struct TrPads {
 };
 
 static __global__ void __launch_bounds__(256) evo_tr_pad_kernel(const TrPads p) {
+    ptx::pdl_launch();
+    ptx::pdl_wait();
     const int lane = threadIdx.x & 31;
     int k = 0;
     long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -944,6 +950,8 @@ struct TrReduceParams {
 
 template <typename T>
 __global__ void __launch_bounds__(256) evo_tr_mma_reduce_kernel(const TrReduceParams<T> p) {
+    ptx::pdl_launch();
+    ptx::pdl_wait();
     const int w = blockIdx.z, n = (blockIdx.y * 64 + (threadIdx.x & 63)) * 4, r = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (p.out[w] == nullptr || r >= p.R[w] || n >= p.N[w]) return;
     const size_t slot = size_t(p.R[w]) * p.ld[w];
