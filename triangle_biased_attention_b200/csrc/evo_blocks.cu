@@ -208,6 +208,15 @@ bool launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t s
 
 unsigned blocks_of(int64_t n, int64_t tile) { return unsigned((n + tile - 1) / tile); }
 
+// Y or dX of one chunk.
+template <bool BWD>
+bool launch_simt_out(const evo::TrSimtParams& p, cudaStream_t st) {
+    const unsigned mt = blocks_of(p.rows, 128);
+    if (int64_t(blocks_of(p.C, 128)) * mt < 2 * 148)
+        return launch(evo::evo_tr_simt_out_kernel<BWD, 1>, dim3(blocks_of(p.C, 64), mt), evo::kTrThreads, kTrSmem, st, p);
+    return launch(evo::evo_tr_simt_out_kernel<BWD, 2>, dim3(blocks_of(p.C, 128), mt), evo::kTrThreads, kTrSmem, st, p);
+}
+
 template <int ACT>
 int run_fwd_simt(const float* X, const float* Wg, const float* Wu, const float* Wd, float* Y, char* ws, int64_t M, int64_t C, int64_t F,
                  int dtype, cudaStream_t st) {
@@ -228,7 +237,7 @@ int run_fwd_simt(const float* X, const float* Wg, const float* Wu, const float* 
         p.out = Y + m * C;
         const unsigned mt = blocks_of(p.rows, 128);
         if (!launch(evo::evo_tr_simt_gate_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
-            !launch(evo::evo_tr_simt_out_kernel<false>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem, st, p))
+            !launch_simt_out<false>(p, st))
             return EVO_ERR_CUDA;
     }
     return EVO_OK;
@@ -262,8 +271,7 @@ int run_bwd_simt(const float* X, const float* Wg, const float* Wu, const float* 
         p.first = m == 0;
         const unsigned mt = blocks_of(p.rows, 128), big = blocks_of(std::max(C, F), 128);
         if (!launch(evo::evo_tr_simt_grad_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
-            (dX && !launch(evo::evo_tr_simt_out_kernel<true>, dim3(blocks_of(C, 128), mt), evo::kTrThreads, kTrSmem,
-                           st, p)) ||
+            (dX && !launch_simt_out<true>(p, st)) ||
             (p.dw_mask && !launch(evo::evo_tr_simt_dw_kernel, dim3(big, big, unsigned(3 * L.splits)),
                                   evo::kTrThreads, kTrSmem, st, p)))
             return EVO_ERR_CUDA;

@@ -39,25 +39,38 @@ __device__ __forceinline__ TrOperand tr_rows(const float* p, long long row_strid
     return o;
 }
 
-// This thread's 8 elements of a 128 x 16 slab.  K-contiguous: 8 k of one row;
-// else 8 rows of one k.
+// This thread's share of an operand's 128 x 16 slabs.  K-contiguous: 8 k of one
+// row; else 8 rows of one k.
 template <bool KC>
-__device__ __forceinline__ void tr_fetch(float (&v)[8], const TrOperand& o, int k0, int kend, bool vec) {
-    const int t = threadIdx.x;
-    const int row = KC ? (t >> 1) : (t & 15) * 8;
-    const int k = k0 + (KC ? (t & 1) * 8 : (t >> 4));
-    const int h = row >> 6, r = row & 63;
-    const float* p = KC ? o.p[h] + r * o.ld + k : o.p[h] + (long long)k * o.ld + r;
-    const int n = KC ? (r < o.lim[h] ? kend - k : 0) : (k < kend ? o.lim[h] - r : 0);  // elements in range
-    if (vec && n >= 8) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        return;
+struct TrFetch {
+    const float* p;  // its first element of the next slab
+    long long step;  // to the next slab
+    int k, rows;     // that slab's k; rows in range from its own on
+
+    __device__ __forceinline__ TrFetch(const TrOperand& o, int kbeg) {
+        const int t = threadIdx.x, row = KC ? (t >> 1) : (t & 15) * 8, r = row & 63;
+        const bool second = row >= 64;
+        const float* base = second ? o.p[1] : o.p[0];
+        k = kbeg + (KC ? (t & 1) * 8 : (t >> 4));
+        rows = (second ? o.lim[1] : o.lim[0]) - r;
+        p = KC ? base + r * o.ld + k : base + (long long)k * o.ld + r;
+        step = KC ? kTrK : kTrK * o.ld;
     }
+
+    __device__ __forceinline__ void load(float (&v)[8], int kend, bool vec) {
+        const int n = KC ? (rows > 0 ? kend - k : 0) : (k < kend ? rows : 0);  // elements in range
+        if (vec && n >= 8) {
+            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
-}
+            for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
+        }
+        p += step;
+        k += kTrK;
+    }
+};
 
 template <bool KC>
 __device__ __forceinline__ void tr_put(float* s, const float (&v)[8]) {
@@ -87,10 +100,12 @@ __device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOper
     constexpr int SLAB = kTrK * kTrLd;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float va[8], vb[8];
+    TrFetch<AKC> fa(A, kbeg);
+    TrFetch<BKC> fb(B, kbeg);
     __syncthreads();  // an earlier product's slabs are no longer read
     if (kbeg < kend) {
-        tr_fetch<AKC>(va, A, kbeg, kend, vec);
-        tr_fetch<BKC>(vb, B, kbeg, kend, vec);
+        fa.load(va, kend, vec);
+        fb.load(vb, kend, vec);
         tr_put<AKC>(smem, va);
         tr_put<BKC>(smem + SLAB, vb);
     }
@@ -99,8 +114,8 @@ __device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOper
     for (int k0 = kbeg; k0 < kend; k0 += kTrK) {
         const bool more = k0 + kTrK < kend;
         if (more) {
-            tr_fetch<AKC>(va, A, k0 + kTrK, kend, vec);
-            tr_fetch<BKC>(vb, B, k0 + kTrK, kend, vec);
+            fa.load(va, kend, vec);
+            fb.load(vb, kend, vec);
         }
         const float* sa = smem + 2 * cur * SLAB;
         const float* sb = sa + SLAB;
@@ -163,7 +178,7 @@ struct TrSimtParams {
 
 // H = act(X Wg^T) * (X Wu^T): 128 rows x 64 features a block.
 template <int ACT>
-__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_gate_kernel(const TrSimtParams p) {
+__global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_gate_kernel(const TrSimtParams p) {
     extern __shared__ __align__(16) float tr_smem[];
     const int f0 = blockIdx.x * 64, m0 = blockIdx.y * 128;
     const TrOperand A = tr_rows(p.x, p.C, p.C, m0, p.rows);
@@ -187,27 +202,29 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_gate_kernel(const TrSi
     }
 }
 
-// Y = H Wd^T (BWD false), or dX = dG Wg + dU Wu: 128 rows x 128 channels a block.
-template <bool BWD>
-__global__ void __launch_bounds__(kTrThreads) evo_tr_simt_out_kernel(const TrSimtParams p) {
+// Y = H Wd^T (BWD false), or dX = dG Wg + dU Wu: 128 rows x 64 * COLS channels a
+// block (64 where 128 would leave SMs without two blocks).
+template <bool BWD, int COLS>
+__global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_out_kernel(const TrSimtParams p) {
     extern __shared__ __align__(16) float tr_smem[];
-    const int c0 = blockIdx.x * 128, m0 = blockIdx.y * 128;
-    float2 acc[8][4] = {};
+    const int c0 = blockIdx.x * 64 * COLS, m0 = blockIdx.y * 128;
+    float2 acc[8][2 * COLS] = {};
+    const int c_end = min(p.C, c0 + 64 * COLS);
     if constexpr (BWD) {
-        tr_tile<true, false, 2>(acc, tr_rows(p.dg, p.F, p.F, m0, p.rows), tr_rows(p.wg, 1, p.C, c0, p.C), 0, p.F,
-                                   p.vec, tr_smem);
-        tr_tile<true, false, 2>(acc, tr_rows(p.du, p.F, p.F, m0, p.rows), tr_rows(p.wu, 1, p.C, c0, p.C), 0, p.F,
-                                   p.vec, tr_smem);
+        tr_tile<true, false, COLS>(acc, tr_rows(p.dg, p.F, p.F, m0, p.rows), tr_rows(p.wg, 1, p.C, c0, c_end), 0, p.F, p.vec,
+                                   tr_smem);
+        tr_tile<true, false, COLS>(acc, tr_rows(p.du, p.F, p.F, m0, p.rows), tr_rows(p.wu, 1, p.C, c0, c_end), 0, p.F, p.vec,
+                                   tr_smem);
     } else {
-        tr_tile<true, true, 2>(acc, tr_rows(p.h, p.F, p.F, m0, p.rows), tr_rows(p.wd, p.F, p.F, c0, p.C), 0, p.F,
-                                  p.vec, tr_smem);
+        tr_tile<true, true, COLS>(acc, tr_rows(p.h, p.F, p.F, m0, p.rows), tr_rows(p.wd, p.F, p.F, c0, c_end), 0, p.F, p.vec,
+                                  tr_smem);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int m = m0 + tr_row(i);
         if (m >= p.rows) continue;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < COLS; ++g) {
             const int c = c0 + tr_col(g, 0);
             const float v[4] = {acc[i][2 * g].x, acc[i][2 * g].y, acc[i][2 * g + 1].x, acc[i][2 * g + 1].y};
             tr_store4(p.out + (long long)m * p.C + c, v, p.C - c, p.vec);
@@ -258,7 +275,7 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_grad_kernel(const TrSi
 // Partial weight gradients of one range of rows: dG^T X, dU^T X [F, C] and
 // dY^T H [C, F], summed into this range's own slot (chunks of rows run one after
 // another, so each slot is added to in a fixed order: no atomics).
-static __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_dw_kernel(const TrSimtParams p) {
+static __global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_dw_kernel(const TrSimtParams p) {
     extern __shared__ __align__(16) float tr_smem[];
     const int which = blockIdx.z % 3, split = blockIdx.z / 3;
     if (!((p.dw_mask >> which) & 1)) return;
