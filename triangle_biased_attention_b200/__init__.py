@@ -20,6 +20,7 @@ fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -488,6 +489,12 @@ class _OnStream:
             self.scope.__exit__(*exc)
 
 
+# workspace bytes are a function of the sizes alone
+_transition_fwd_bytes = functools.lru_cache(maxsize=1024)(evo_transition_fwd_workspace_size)
+_transition_bwd_bytes = functools.lru_cache(maxsize=1024)(evo_transition_bwd_workspace_size)
+_relpos_bwd_bytes = functools.lru_cache(maxsize=1024)(evo_relpos_bwd_workspace_size)
+
+
 def _workspace(workspace: Optional[torch.Tensor], need: int, device, what: str) -> torch.Tensor:
     if need < 0:
         raise EvoAttnError(need, what)
@@ -511,8 +518,10 @@ def _transition_args(x, w_gate, w_up, w_down, act):
     if w_gate.dim() != 2:
         raise ValueError("w_gate must be [F, C]")
     F = w_gate.shape[0]
-    for name, t, shape in (("w_gate", w_gate, (F, C)), ("w_up", w_up, (F, C)), ("w_down", w_down, (C, F))):
-        _same(name, t, shape, x.dtype, x.device)
+    dtype, device = x.dtype, x.device
+    _same("w_gate", w_gate, (F, C), dtype, device)
+    _same("w_up", w_up, (F, C), dtype, device)
+    _same("w_down", w_down, (C, F), dtype, device)
     M = 1
     for n in x.shape[:-1]:
         M *= n
@@ -540,7 +549,7 @@ def transition(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down
             out = torch.empty_like(x)
         else:
             _same("out", out, x.shape, x.dtype, x.device)
-        workspace = _workspace(workspace, evo_transition_fwd_workspace_size(M, C, F, code), x.device,
+        workspace = _workspace(workspace, _transition_fwd_bytes(M, C, F, code), x.device,
                                "evo_transition_fwd_workspace_size")
     status = evo_transition_fwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), out.data_ptr(),
                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), M, C, F, _ACTS[act],
@@ -569,7 +578,7 @@ def transition_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tenso
     with on:
         dx = torch.empty_like(x) if need_dx else None
         dw = [torch.empty_like(w) for w in (w_gate, w_up, w_down)] if need_dw else [None] * 3
-        workspace = _workspace(workspace, evo_transition_bwd_workspace_size(M, C, F, code), x.device,
+        workspace = _workspace(workspace, _transition_bwd_bytes(M, C, F, code), x.device,
                                "evo_transition_bwd_workspace_size")
     status = evo_transition_bwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), dy.data_ptr(),
                                 _ptr(dx), _ptr(dw[0]), _ptr(dw[1]), _ptr(dw[2]), workspace.data_ptr(),
@@ -622,12 +631,16 @@ def _relpos_args(borders, pos, pos_k, chain, chain_k, device):
         raise ValueError("chain and chain_k must be given together")
     if borders.dim() != 1 or pos_k.dim() != 2:
         raise ValueError("borders must be [num_borders] and pos_k [B, Sk]")
-    B, Sq, Sk = pos.shape[0], pos.shape[1], pos_k.shape[1]
-    for name, t, shape in (("borders", borders, borders.shape), ("pos", pos, (B, Sq)), ("pos_k", pos_k, (B, Sk)),
-                           ("chain", chain, (B, Sq)), ("chain_k", chain_k, (B, Sk))):
-        if t is not None:
-            _same(name, t, shape, torch.int32, device)
-    return pos_k, chain_k, B, Sq, Sk, borders.shape[0]
+    B, Sq = pos.shape
+    nb, Sk = borders.shape[0], pos_k.shape[1]
+    _same("borders", borders, (nb,), torch.int32, device)
+    _same("pos", pos, (B, Sq), torch.int32, device)
+    if pos_k is not pos:
+        _same("pos_k", pos_k, (B, Sk), torch.int32, device)
+    if chain is not None:
+        _same("chain", chain, (B, Sq), torch.int32, device)
+        _same("chain_k", chain_k, (B, Sk), torch.int32, device)
+    return pos_k, chain_k, B, Sq, Sk, nb
 
 
 def relpos_bias(table: torch.Tensor, borders: torch.Tensor, pos: torch.Tensor, pos_k: Optional[torch.Tensor] = None,
@@ -690,7 +703,7 @@ def relpos_bias_backward(dpair: torch.Tensor, borders: torch.Tensor, pos: torch.
     has_chain = chain is not None
     with on:
         dtable = torch.empty((nb + 1 + has_chain, H), dtype=dpair.dtype, device=dpair.device)
-        workspace = _workspace(workspace, evo_relpos_bwd_workspace_size(B, Sq, Sk, H, nb, int(has_chain)), dpair.device,
+        workspace = _workspace(workspace, _relpos_bwd_bytes(B, Sq, Sk, H, nb, int(has_chain)), dpair.device,
                                "evo_relpos_bwd_workspace_size")
     status = evo_relpos_bwd(dpair.data_ptr(), borders.data_ptr(), pos.data_ptr(), pos_k.data_ptr(), _ptr(chain),
                             _ptr(chain_k), dtable.data_ptr(), workspace.data_ptr(),
