@@ -60,9 +60,11 @@ def test_both_activations(act, dt):
     check(*make(200, 96, 160, dt, seed=5), act, f"{act} {dt}")
 
 
-def test_more_rows_than_one_chunk():
-    """Rows are taken in chunks; the weight gradients add up over them."""
-    M, C, F = 4 * 18944 + 300, 16, 1200
+@pytest.mark.parametrize("waves,C,F", [(5, 16, 1200), (3, 136, 1200)])
+def test_more_rows_than_one_chunk(waves, C, F):
+    """Rows are taken in chunks (of whole waves of 148 128-row tiles); the weight
+    gradients add up over them."""
+    M = waves * 18944 + 300
     assert evo.evo_transition_bwd_workspace_size(M, C, F, evo.EVO_DTYPE_BF16) == \
         evo.evo_transition_bwd_workspace_size(M + 18944, C, F, evo.EVO_DTYPE_BF16)
     check(*make(M, C, F, BF16, seed=1), "silu", f"chunks {M}")

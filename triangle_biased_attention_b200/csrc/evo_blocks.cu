@@ -90,6 +90,7 @@ struct TrLayout {
     int64_t part = 0, part2 = 0, part3 = 0;       // partial weight gradients, fp32: [splits][R][N up to 4] (fp32 call: one)
     bool direct = false;                          // 16-bit: the last products are the weight gradients
     int64_t splits = 0, split_rows = 0;           // ranges of rows with a slot of their own
+    bool gradw = false;                           // the backward that keeps weight gradients on chip: no H, [C, F up to 64] slots
     bool few = false;                             // the forward's form for a few rows: H [M, F] in fp32
     bool fused = false;                           // the forward's one-kernel form: no [M, F] array at all
     int64_t x = 0, dy = 0, wg = 0, wu = 0, wd = 0;  // 16-bit, odd C or F: copies with rows of whole 16-byte units
@@ -106,6 +107,10 @@ bool tr_few(int64_t M, int64_t C, int64_t F) {
 // gives a tile of rows to one SM, so it wants tiles for most of them.
 bool tr_fused(int64_t M, int64_t C, int dtype) { return dtype != EVO_DTYPE_FP32 && C <= 256 && M > 64 * 128; }
 
+// The backward that holds 64 features' weight gradients in tensor memory: 128
+// channels in its lanes, and row tiles to share out.
+bool tr_gradw(int64_t M, int64_t C, int dtype) { return dtype != EVO_DTYPE_FP32 && C <= 128 && M > 64 * 128; }
+
 // Sections on 256-byte boundaries.  False when a byte count passes int64.
 bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayout* L) {
     const int64_t es = elem_bytes(dtype);
@@ -120,9 +125,10 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
     const int64_t ldf = dtype == EVO_DTYPE_FP32 ? F : round_up(F, 128);
     L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
     L->fused = !backward && tr_fused(M, C, dtype);
+    L->gradw = backward && tr_gradw(M, C, dtype);
     // (the one-kernel forward needs chunks only for the copy of X)
     L->chunk = L->fused ? (L->pad ? tr_chunk_rows(M, round_up(C, 8) * 2, false) : M)
-                        : tr_chunk_rows(M, ldf * es * (backward ? 3 : 1), backward);
+                        : tr_chunk_rows(M, ldf * es * (backward ? (L->gradw ? 2 : 3) : 1), backward);
     const int64_t hbytes = (dtype == EVO_DTYPE_FP32 ? L->chunk : round_up(L->chunk, 128)) * ldf * es;
     int64_t off = 0;
     auto take = [&off](int64_t bytes) {
@@ -130,7 +136,7 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
         off += round_up(bytes, 256);
         return at;
     };
-    if (!L->fused) L->h = take(hbytes);
+    if (!L->fused && !L->gradw) L->h = take(hbytes);
     if (backward) {
         L->dg = take(hbytes);
         L->du = take(hbytes);
@@ -140,6 +146,9 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
             L->splits = std::max<int64_t>(1, std::min((296 + tiles - 1) / tiles, (L->chunk + 511) / 512));
             L->split_rows = (L->chunk + L->splits - 1) / L->splits;
             L->part = take(L->splits * 3 * fc * 4);
+        } else if (L->gradw) {
+            L->splits = std::max<int64_t>(1, 148 / ((F + 63) / 64));
+            L->part = take(3 * L->splits * C * round_up(F, 64) * 4);
         } else {
             // as many ranges as keep the tiles within one wave of 148 SMs, none under 512 rows
             const int64_t bn = C > 128 ? 256 : 128;
@@ -463,6 +472,39 @@ bool encode_slots(CUtensorMap* m, void* base, int64_t splits, int64_t R, int64_t
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// dG, dU and the weight gradients' sums of one chunk (C <= 128), with the maps of GRAD and DX.
+template <int ACT, bool F16>
+int launch_gradw(int dev, const evo::TrMaps& grad, const evo::TrMaps& dx, const TrLayout& L, char* ws, bool need_dx, int rows,
+                 bool first, int64_t C, int64_t F, cudaStream_t st) {
+    using Cfg = evo::TrGradwCfg<F16>;
+    auto kernel = evo::evo_tr_gradw_kernel<ACT, F16>;
+    static AttrOnce attr;
+    if (!attr.ensure(dev, kernel, Cfg::SMEM_BYTES)) return EVO_ERR_CUDA;
+    evo::TrGradwParams p = {};
+    p.d[0] = need_dx ? reinterpret_cast<uint16_t*>(ws + L.dg) : nullptr;
+    p.d[1] = need_dx ? reinterpret_cast<uint16_t*>(ws + L.du) : nullptr;
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.ldf = int(round_up(F, 128));
+    p.ldp = int(round_up(F, 64));
+    p.M = rows;
+    p.C = int(C);
+    p.F = int(F);
+    p.num_tiles = tiles_of(rows, 128);
+    p.kc = tiles_of(C, 64);
+    p.slices = tiles_of(F, Cfg::FC);
+    p.splits = int(L.splits);
+    p.first = first;
+    evo::TrMaps a;  // X, dY, Wg, Wu (boxes of 64 rows), Wd
+    std::memset(&a, 0, sizeof(a));
+    a.m[0] = grad.m[0];
+    a.m[1] = grad.m[3];
+    a.m[2] = dx.m[1];
+    a.m[3] = dx.m[3];
+    a.m[4] = grad.m[4];
+    return launch_dependent(kernel, dim3(unsigned(p.slices * p.splits)), Cfg::THREADS, Cfg::SMEM_BYTES, st, a, p) ? EVO_OK
+                                                                                                                : EVO_ERR_CUDA;
+}
+
 template <bool F16, int ACT>
 int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const void* Wd, const void* dY, void* dX,
                 void* dWg, void* dWu, void* dWd, char* ws, int64_t M, int64_t C, int64_t F, int dtype, cudaStream_t st) {
@@ -513,7 +555,7 @@ int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
             return EVO_ERR_CUDA;
         for (int w = 0; w < 3; ++w) {
             const int64_t R = w == 2 ? C : F, N = w == 2 ? F : C;
-            if (dw[w] && !(L.direct ? encode_rows(&wgt.m[5 + w], dw[w], R, N, N, 32, F16, 32)
+            if (dw[w] && !L.gradw && !(L.direct ? encode_rows(&wgt.m[5 + w], dw[w], R, N, N, 32, F16, 32)
                                     : encode_slots(&wgt.m[5 + w], part[w], L.splits, R, N)))
                 return EVO_ERR_CUDA;
         }
@@ -521,14 +563,27 @@ int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
         p.tiles_n = tiles_of(F, 128);
         p.num_tiles = p.tiles_m * p.tiles_n;
         p.kb = tiles_of(C, 64);
-        if (launch_mma<evo::TR_GRAD, ACT, F16, 256>(dev, sms, grad, p, st) != EVO_OK) return EVO_ERR_CUDA;
+        if (L.gradw) {
+            if (launch_gradw<ACT, F16>(dev, grad, out, L, ws, dX != nullptr, p.rows, m == 0, C, F, st) != EVO_OK)
+                return EVO_ERR_CUDA;
+        } else if (launch_mma<evo::TR_GRAD, ACT, F16, 256>(dev, sms, grad, p, st) != EVO_OK) {
+            return EVO_ERR_CUDA;
+        }
         if (dX && launch_out<evo::TR_DX, F16>(dev, sms, out, p, static_cast<uint16_t*>(dX) + m * C, st) != EVO_OK)
             return EVO_ERR_CUDA;
-        if (p.num_which > 0) {
+        if (p.num_which > 0 && !L.gradw) {
             p.num_tiles = dw_tiles;
             p.tiles_n = int(L.splits);
             if (launch_mma<evo::TR_DW, 0, F16, 256>(dev, sms, wgt, p, st) != EVO_OK) return EVO_ERR_CUDA;
         }
+    }
+    if (L.gradw) {
+        if (p.num_which > 0 &&
+            !launch_dependent(evo::evo_tr_gradw_reduce_kernel<T>, dim3(blocks_of(F, 32), blocks_of(C, 8), 3), 256, 0, st,
+                              reinterpret_cast<const float*>(ws + L.part), int(L.splits), p.C, p.F, int(round_up(F, 64)),
+                              static_cast<T*>(dWg), static_cast<T*>(dWu), static_cast<T*>(dWd)))
+            return EVO_ERR_CUDA;
+        return EVO_OK;
     }
     if (p.num_which > 0 && !L.direct) {
         evo::TrReduceParams<T> r = {};

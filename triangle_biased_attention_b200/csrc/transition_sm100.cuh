@@ -908,6 +908,309 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
     if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
+// -------------------------------- dG, dU and the weight gradients in one kernel
+
+// For C <= 128 the three arrays [M, F] that GRAD writes and DW reads outweigh
+// everything else (147456 rows x 512 features: 0.9 GB, 138 us at the copy rate).
+// Here a CTA owns 64 features and a share of the row tiles: the features' weights
+// stay in shared memory, and the gradients of these weights stay in tensor memory
+// over all its tiles, 192 columns ([X^T dG | X^T dU] and dY^T H, channels in the
+// lanes).  H is never written, dG and dU only for dX's product.
+//
+// Per row tile: X and dY arrive once (two buffers of 64 KB) and serve G, U and dH
+// K-major and the weight gradients MN-major; eight warps turn G, U, dH (192
+// columns, G and U twice) into tiles of dG, dU and H in shared memory.  Warp 1
+// issues G, U and dH, warp 2 the weight gradients.
+struct TrGradwParams {
+    uint16_t* d[2];  // dG, dU [M, ldf], or null where dX is not asked for
+    float* part;     // [3][splits][C][ldp]: dWg^T, dWu^T, dWd of each share of the rows
+    int ldf, ldp;
+    int M, C, F;
+    int num_tiles;   // ceil(M / 128)
+    int kc;          // 64-deep blocks of C: 1 or 2
+    int slices;      // ceil(F / 64)
+    int splits;
+    int first;       // the slots start here
+};
+
+template <bool F16>
+struct TrGradwCfg {
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+    static constexpr int FC = 64;
+    static constexpr int XBUF = 65536;             // X's blocks (128 rows x 64 k, 16 KB each), dY's from 32768
+    static constexpr int OFF_W = 2 * XBUF;         // Wg, Wu of each block (8 KB each), Wd's blocks from 32768
+    static constexpr int OFF_D = OFF_W + 49152;    // dG, dU, H: 128 rows x 64 features each
+    static constexpr int OFF_BAR = OFF_D + 49152;
+    static constexpr int WF = 0, XF = 1, XE = XF + 2, GF = XE + 2, GE = GF + 2, DF = GE + 2, DE = DF + 1, OF = DE + 1,
+                         DRAIN = OF + 1, NUM_BARS = DRAIN + 2;
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    // G, U: 128 columns from 0 and from 128; dH: 256; X^T dG, X^T dU: 320; dY^T H: 448
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t AB = F16 ? 0u : ((1u << 7) | (1u << 10));
+    __host__ __device__ static constexpr uint32_t idesc(bool a_mn, bool b_mn, int n) {
+        return (1u << 4) | AB | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t(n) >> 3) << 17) |
+               ((128u >> 4) << 24);
+    }
+};
+
+// maps: X, dY (boxes of 128 rows), Wg, Wu, Wd (64 rows)
+template <int ACT, bool F16>
+__global__ void __launch_bounds__(384, 1)
+evo_tr_gradw_kernel(const __grid_constant__ TrMaps maps, const TrGradwParams p) {
+    using C = TrGradwCfg<F16>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = ptx::smem_u32(smem);
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
+    auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8u * uint32_t(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    const int slice = int(blockIdx.x) % p.slices, split = int(blockIdx.x) / p.slices;
+    const int total = (p.num_tiles - split + p.splits - 1) / p.splits;  // row tiles split, split + splits, ...
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NUM_BARS; ++i)
+            ptx::mbar_init(bar(i), i == C::GE || i == C::GE + 1 || i == C::DF ? C::EPI_WARPS : 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    ptx::pdl_launch();
+    ptx::pdl_wait();
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- loads
+        if (lane == 0 && total > 0) {
+            const uint32_t d = sb + uint32_t(C::OFF_W), f = bar(C::WF);
+            ptx::mbar_arrive_expect_tx(f, uint32_t(p.kc) * 24576u);
+            for (int k = 0; k < p.kc; ++k) {
+                ptx::tma_load_2d(d + 16384 * k, &maps.m[2], f, 64 * k, C::FC * slice);
+                ptx::tma_load_2d(d + 16384 * k + 8192, &maps.m[3], f, 64 * k, C::FC * slice);
+                ptx::tma_load_2d(d + 32768 + 8192 * k, &maps.m[4], f, C::FC * slice, 64 * k);
+            }
+        }
+        __syncwarp();
+        bool ok = true;
+        int q = 0;
+        for (; q < total; ++q) {
+            const int b = q & 1;
+            ok = wait_warp(bar(C::XE + b), uint32_t((q >> 1) & 1) ^ 1u, abort_flag);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t d = sb + uint32_t(C::XBUF * b), f = bar(C::XF + b);
+                const int m = 128 * (split + q * p.splits);
+                ptx::mbar_arrive_expect_tx(f, uint32_t(p.kc) * 32768u);
+                for (int k = 0; k < p.kc; ++k) {
+                    ptx::tma_load_2d(d + 16384 * k, &maps.m[0], f, 64 * k, m);
+                    ptx::tma_load_2d(d + 32768 + 16384 * k, &maps.m[1], f, 64 * k, m);
+                }
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) {
+            // the last load of each buffer lands before the CTA exits
+            wait_bounded(bar(C::WF), 0u, nullptr);
+            for (int b = 0; b < 2; ++b)
+                if (q - 1 >= b) wait_bounded(bar(C::XF + b), uint32_t((q - 1 - b) / 2) & 1u, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------- G, U, dH products
+        bool ok = total == 0 || wait_warp(bar(C::WF), 0u, abort_flag), issued = false;
+        const uint32_t w = sb + uint32_t(C::OFF_W);
+        for (int q = 0; q < total && ok; ++q) {
+            const int b = q & 1;
+            const uint32_t ph = uint32_t(q >> 1) & 1u, x = sb + uint32_t(C::XBUF * b);
+            ok = wait_warp(bar(C::GE + b), ph ^ 1u, abort_flag);  // G and U of tile q - 2 have been read
+            if (!ok) break;
+            ok = wait_warp(bar(C::XF + b), ph, abort_flag);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            for (int k = 0; k < p.kc; ++k)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_ss_elect(tmem + 128u * uint32_t(b), desc_k_major<128>(x + 16384 * k + 32 * kk),
+                                      desc_k_major<128>(w + 16384 * k + 32 * kk), C::idesc(false, false, 128),
+                                      (k > 0 || kk > 0) ? 1u : 0u);
+            issued = true;
+            if (q > 0) {  // and dH of tile q - 1
+                ok = wait_warp(bar(C::GE + (b ^ 1)), uint32_t((q - 1) >> 1) & 1u, abort_flag);
+                if (!ok) break;
+                ptx::tc_fence_after();
+            }
+            for (int k = 0; k < p.kc; ++k)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_ss_elect(tmem + 256u, desc_k_major<128>(x + 32768 + 16384 * k + 32 * kk),
+                                      desc_mn_major<128>(w + 32768 + 8192 * k + 2048 * kk, 8192), C::idesc(false, true, 64),
+                                      (k > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_commit_elect(bar(C::GF + b));
+        }
+        if (!ok && issued) {
+            ptx::mma_commit_elect(bar(C::DRAIN));
+            wait_bounded(bar(C::DRAIN), 0, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------ weight gradients
+        bool ok = true, issued = false;
+        const uint32_t d = sb + uint32_t(C::OFF_D);
+        for (int q = 0; q < total && ok; ++q) {
+            const int b = q & 1;
+            // the tiles are in place, so X and dY landed long ago
+            ok = wait_warp(bar(C::DF), uint32_t(q) & 1u, abort_flag);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t x = sb + uint32_t(C::XBUF * b), add = q > 0 ? 1u : 0u;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // 16 rows
+                ptx::mma_ss_elect(tmem + 320u, desc_mn_major<128>(x + 2048 * kk, 16384), desc_mn_major<128>(d + 2048 * kk, 16384),
+                                  C::idesc(true, true, 128), kk > 0 ? 1u : add);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                ptx::mma_ss_elect(tmem + 448u, desc_mn_major<128>(x + 32768 + 2048 * kk, 16384),
+                                  desc_mn_major<128>(d + 32768 + 2048 * kk, 16384), C::idesc(true, true, 64), kk > 0 ? 1u : add);
+            issued = true;
+            ptx::mma_commit_elect(bar(C::XE + b));
+            ptx::mma_commit_elect(bar(C::DE));
+        }
+        if (ok) ptx::mma_commit_elect(bar(C::OF));
+        if (!ok && issued) {
+            ptx::mma_commit_elect(bar(C::DRAIN + 1));
+            wait_bounded(bar(C::DRAIN + 1), 0, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------- activations
+        const int wq = warp & 3, half = (warp - 4) >> 2;
+        const int r = 32 * wq + lane;
+        const uint32_t tl = tmem + (uint32_t(32 * wq) << 16), dt = sb + uint32_t(C::OFF_D);
+        bool ok = true;
+        for (int q = 0; q < total && ok; ++q) {
+            const int b = q & 1;
+            ok = wait_warp(bar(C::GF + b), uint32_t(q >> 1) & 1u, abort_flag);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            float g[32], u[32], d[32];
+            ptx::tmem_ld_x32(tl + uint32_t(128 * b + 32 * half), reinterpret_cast<uint32_t*>(g));
+            ptx::tmem_ld_x32(tl + uint32_t(128 * b + 64 + 32 * half), reinterpret_cast<uint32_t*>(u));
+            ptx::tmem_ld_x32(tl + uint32_t(256 + 32 * half), reinterpret_cast<uint32_t*>(d));
+            ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
+            ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
+            ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(d));
+            ptx::tc_fence_before();
+            ptx::mbar_arrive_elect(bar(C::GE + b));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float2 hv, dgv, duv;
+                tr_grad2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]),
+                              make_float2(d[2 * e], d[2 * e + 1]), hv, dgv, duv);
+                d[2 * e] = hv.x, d[2 * e + 1] = hv.y;
+                g[2 * e] = dgv.x, g[2 * e + 1] = dgv.y;
+                u[2 * e] = duv.x, u[2 * e + 1] = duv.y;
+            }
+            // the products of the tile before have read its dG, dU and H
+            ok = wait_warp(bar(C::DE), uint32_t(q & 1) ^ 1u, abort_flag);
+            if (!ok) break;
+#pragma unroll
+            for (int o = 0; o < 3; ++o) {
+                const float* v = o == 0 ? g : o == 1 ? u : d;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    ptx::st_shared_v4(dt + uint32_t(16384 * o) + swz_chunk<128>(r, 4 * half + e),
+                                      make_uint4(tr_pack<F16>(v[8 * e], v[8 * e + 1]), tr_pack<F16>(v[8 * e + 2], v[8 * e + 3]),
+                                                 tr_pack<F16>(v[8 * e + 4], v[8 * e + 5]),
+                                                 tr_pack<F16>(v[8 * e + 6], v[8 * e + 7])));
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            ptx::mbar_arrive_elect(bar(C::DF));
+            if (p.d[0] != nullptr) {
+                // this warp's 32 rows x 64 bytes of dG and dU, 8 rows at a time
+                const int m0 = 128 * (split + q * p.splits) + 32 * wq;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    uint16_t* out = p.d[o] + size_t(m0 + (lane >> 2)) * p.ldf + C::FC * slice + 32 * half + 8 * (lane & 3);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = 8 * e + (lane >> 2);
+                        const uint4 v = ptx::ld_shared_v4(dt + uint32_t(16384 * o) + swz_chunk<128>(32 * wq + row, 4 * half + (lane & 3)));
+                        if (m0 + row < p.M) *reinterpret_cast<uint4*>(out + size_t(8 * e) * p.ldf) = v;
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // the sums: this lane's channel, 32 features at a time
+        if (ok && wait_warp(bar(C::OF), 0u, abort_flag)) {
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 3; ++c) {  // half 0: dWg, half 1: dWu, each in two parts; then half of dWd
+                float v[32];
+                const int which = c == 2 ? 2 : half, f = c == 2 ? 32 * half : 32 * c;
+                ptx::tmem_ld_x32(tl + uint32_t(c == 2 ? 448 + 32 * half : 320 + 64 * half + 32 * c), reinterpret_cast<uint32_t*>(v));
+                ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(v));
+                if (r < p.C) {
+                    float4* o = reinterpret_cast<float4*>(p.part + ((size_t(which) * p.splits + split) * p.C + r) * p.ldp +
+                                                          C::FC * slice + f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float4 s = total > 0 ? make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3])
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (!p.first) {
+                            const float4 y = o[e];
+                            s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
+                        }
+                        o[e] = s;
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// The weight gradients from the shares' sums, added in order and rounded to the
+// type, a thread an element: [3][splits][C][ldp], the first two turned into [F, C].
+template <typename T>
+__global__ void __launch_bounds__(256) evo_tr_gradw_reduce_kernel(const float* __restrict__ part, int splits, int C, int F, int ldp,
+                                                                  T* dwg, T* dwu, T* dwd) {
+    ptx::pdl_launch();
+    ptx::pdl_wait();
+    const int which = blockIdx.z, f = blockIdx.x * 32 + (threadIdx.x & 31), c = blockIdx.y * 8 + (threadIdx.x >> 5);
+    T* out = which == 0 ? dwg : which == 1 ? dwu : dwd;
+    if (out == nullptr || c >= C || f >= F) return;
+    const size_t slot = size_t(C) * ldp;
+    const float* x = part + size_t(which) * splits * slot + size_t(c) * ldp + f;
+    float s = 0.0f;
+    int k = 0;
+    for (; k + 8 <= splits; k += 8) {  // eight loads on their way at a time
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = x[(k + e) * slot];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[e];
+    }
+    for (; k < splits; ++k) s += x[k * slot];
+    tr_store(out + (which == 2 ? size_t(c) * F + f : size_t(f) * C + c), s);
+}
+
 // Rows of `w` elements copied to rows of `wp` (w rounded up to 8), for up to five
 // matrices at once, a warp a row: TMA reads rows of whole 16-byte units only.
 // What lies behind column w is never read.
