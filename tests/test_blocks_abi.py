@@ -15,7 +15,7 @@ def lib():
     return evo.load_library()
 
 
-def fwd(M=16, C=32, F=64, act=0, dt=evo.EVO_DTYPE_BF16, Wb=None, **kw):
+def fwd(M=16, C=304, F=64, act=0, dt=evo.EVO_DTYPE_BF16, Wb=None, **kw):
     a = dict(X=1 * FAR, Wg=2 * FAR, Wu=3 * FAR, Wd=4 * FAR, Y=5 * FAR, W=6 * FAR)
     a.update(kw)
     if Wb is None:
@@ -23,7 +23,7 @@ def fwd(M=16, C=32, F=64, act=0, dt=evo.EVO_DTYPE_BF16, Wb=None, **kw):
     return evo.evo_transition_fwd(a["X"], a["Wg"], a["Wu"], a["Wd"], a["Y"], a["W"], Wb, M, C, F, act, dt, None)
 
 
-def bwd(M=16, C=32, F=64, act=0, dt=evo.EVO_DTYPE_BF16, Wb=None, **kw):
+def bwd(M=16, C=304, F=64, act=0, dt=evo.EVO_DTYPE_BF16, Wb=None, **kw):
     a = dict(X=1 * FAR, Wg=2 * FAR, Wu=3 * FAR, Wd=4 * FAR, dY=5 * FAR, dX=6 * FAR, dWg=7 * FAR, dWu=8 * FAR,
              dWd=9 * FAR, W=10 * FAR)
     a.update(kw)
@@ -39,14 +39,18 @@ ACCEPTED = evo.EVO_ERR_INVALID_ARG
 
 def test_transition_workspace_size():
     for size in (evo.evo_transition_fwd_workspace_size, evo.evo_transition_bwd_workspace_size):
-        assert size(16, 32, 64, evo.EVO_DTYPE_BF16) > 0
+        assert size(16, 304, 64, evo.EVO_DTYPE_BF16) > 0
         assert size(-1, 32, 64, 0) == evo.EVO_ERR_INVALID_ARG
         assert size(16, 32, 64, 9) == evo.EVO_ERR_UNSUPPORTED_DTYPE
         assert size(1 << 31, 32, 64, 0) == evo.EVO_ERR_UNSUPPORTED_SHAPE
         assert size(16, (1 << 20) + 1, 64, 0) == evo.EVO_ERR_UNSUPPORTED_SHAPE
         assert size(0, 32, 64, 0) == 0 and size(16, 0, 64, 0) == 0 and size(16, 32, 0, 0) == 0
         # the workspace holds chunks of rows, not all of them
-        assert size(1 << 24, 128, 512, 0) == size(1 << 30, 128, 512, 0) < 1 << 30
+        for C in (128, 304):
+            assert size(1 << 24, C, 512, 0) == size(1 << 30, C, 512, 0) < 1 << 30
+    # the one-kernel forward needs none, and takes a NULL for it
+    assert evo.evo_transition_fwd_workspace_size(1 << 20, 128, 512, evo.EVO_DTYPE_FP16) == 0
+    assert fwd(M=1 << 20, C=128, F=512, W=None, Y=5 * FAR + 2) == evo.EVO_ERR_MISALIGNED
 
 
 @pytest.mark.parametrize("call", [fwd, bwd])
@@ -73,7 +77,7 @@ def test_transition_checks_arguments(call):
 
 
 def test_transition_overlaps_and_workspace():
-    full = evo.evo_transition_fwd_workspace_size(16, 32, 64, 0)
+    full = evo.evo_transition_fwd_workspace_size(16, 304, 64, 0)
     # a short workspace or an overlap is refused like a made-up pointer, so each is checked
     # with an alignment fault behind it that an accepted call would report instead
     assert fwd(Y=5 * FAR + 2, W=6 * FAR) == evo.EVO_ERR_MISALIGNED

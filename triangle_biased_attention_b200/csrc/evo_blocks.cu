@@ -104,12 +104,22 @@ bool tr_few(int64_t M, int64_t C, int64_t F) {
 }
 
 // The one-kernel forward holds Y of 128 rows in tensor memory (C <= 256) and
-// gives a tile of rows to one SM, so it wants tiles for most of them.
-bool tr_fused(int64_t M, int64_t C, int dtype) { return dtype != EVO_DTYPE_FP32 && C <= 256 && M > 64 * 128; }
+// gives a tile of rows to one SM, which walks all features; the two-kernel form
+// spreads the features of few rows over the SMs. Measured in turn, us, one kernel
+// against two: C = 128, F = 512: 2048 rows 8.9 / 8.7, 6000 9.1 / 10.3; F = 1024: 4096
+// rows 13.9 / 12.0, 8192 14.3 / 15.4; C = 64, F = 256: 64 rows 5.4 / 6.6, 12000 6.2 /
+// 9.2; C = 256, F = 512: 8192 rows 13.2 / 11.5, 12000 13.9 / 14.5, 131072 x 1024 168 / 261.
+bool tr_fused(int64_t M, int64_t C, int64_t F, int dtype) {
+    if (dtype == EVO_DTYPE_FP32 || C > 256) return false;
+    const int64_t tiles = (M + 127) / 128, chunks = (F + 127) / 128;
+    return C <= 128 ? tiles >= 8 * (chunks - 2) : tiles > 90;
+}
 
-// The backward that holds 64 features' weight gradients in tensor memory: 128
-// channels in its lanes, and row tiles to share out.
-bool tr_gradw(int64_t M, int64_t C, int dtype) { return dtype != EVO_DTYPE_FP32 && C <= 128 && M > 64 * 128; }
+// The backward that holds 64 features' weight gradients in tensor memory, with up
+// to 128 channels in its lanes. Against GRAD and DW apart, us: C = 128, F = 512: 64
+// rows 16.8 / 15.7, 1024 19.0 / 22.9, 19000 41 / 51, 147456 248 / 305; C = 64, F = 256: 64 rows
+// 11.3 / 12.6, 8192 17.3 / 22.9.
+bool tr_gradw(int64_t C, int dtype) { return dtype != EVO_DTYPE_FP32 && C <= 128; }
 
 // Sections on 256-byte boundaries.  False when a byte count passes int64.
 bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayout* L) {
@@ -124,8 +134,8 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
     }
     const int64_t ldf = dtype == EVO_DTYPE_FP32 ? F : round_up(F, 128);
     L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
-    L->fused = !backward && tr_fused(M, C, dtype);
-    L->gradw = backward && tr_gradw(M, C, dtype);
+    L->fused = !backward && tr_fused(M, C, F, dtype);
+    L->gradw = backward && tr_gradw(C, dtype);
     // (the one-kernel forward needs chunks only for the copy of X)
     L->chunk = L->fused ? (L->pad ? tr_chunk_rows(M, round_up(C, 8) * 2, false) : M)
                         : tr_chunk_rows(M, ldf * es * (backward ? (L->gradw ? 2 : 3) : 1), backward);
@@ -147,7 +157,8 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
             L->split_rows = (L->chunk + L->splits - 1) / L->splits;
             L->part = take(L->splits * 3 * fc * 4);
         } else if (L->gradw) {
-            L->splits = std::max<int64_t>(1, 148 / ((F + 63) / 64));
+            // a share of the row tiles for each SM left by the feature slices
+            L->splits = std::max<int64_t>(1, std::min(148 / ((F + 63) / 64), (L->chunk + 127) / 128));
             L->part = take(3 * L->splits * C * round_up(F, 64) * 4);
         } else {
             // as many ranges as keep the tiles within one wave of 148 SMs, none under 512 rows
