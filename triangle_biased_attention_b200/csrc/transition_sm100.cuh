@@ -102,6 +102,23 @@ __device__ __forceinline__ float2 tr_add2(float2 a, float2 b) {
     return d;
 }
 
+__device__ __forceinline__ float2 tr_mad2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+          "l"(reinterpret_cast<const unsigned long long&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 tr_both(float v) { return make_float2(v, v); }
+
+// 1 / a of two elements with one reciprocal; a.x * a.y must be finite
+__device__ __forceinline__ float2 tr_rcp2(float2 a) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a.x * a.y));
+    return tr_mul2(tr_both(r), make_float2(a.y, a.x));
+}
+
 // sigmoid of two elements.  One reciprocal serves both: 1/a = b / (a b), which
 // leaves the special-function unit 1.5 instructions an element instead of 2.
 // The exponent is held at 2^60 so that a b stays finite: below g = -41 the
@@ -109,25 +126,26 @@ __device__ __forceinline__ float2 tr_add2(float2 a, float2 b) {
 __device__ __forceinline__ float2 tr_sigmoid2(float2 g) {
     const float2 x = tr_mul2(g, make_float2(-kLog2e, -kLog2e));
     const float2 e = make_float2(ptx::ex2_approx(fminf(x.x, 60.0f)), ptx::ex2_approx(fminf(x.y, 60.0f)));
-    const float2 a = tr_add2(e, make_float2(1.0f, 1.0f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a.x * a.y));
-    return tr_mul2(make_float2(r, r), make_float2(a.y, a.x));
+    return tr_rcp2(tr_add2(e, tr_both(1.0f)));
 }
 
-// Phi(g) and e^(-g^2/2): the complementary error function by Abramowitz and
-// Stegun's formula 7.1.26 (absolute error at most 1.5e-7, below the rounding of
-// a 16-bit result and of the same size as the fp32 error of g itself).
-__device__ __forceinline__ float tr_phi(float g, float& e) {
-    const float x = fabsf(g) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    e = ptx::ex2_approx(-kLog2e * x * x);
-    const float half = 0.5f * p * t * e;  // Phi(-|g|)
-    return g >= 0.0f ? 1.0f - half : half;
+// Phi(g) and e^(-g^2/2) of two elements: the complementary error function by
+// Abramowitz and Stegun's formula 7.1.26 (absolute error at most 1.5e-7, below the
+// rounding of a 16-bit result and of the same size as the fp32 error of g itself).
+// |g| is held at 2^40, where the exponential has long been 0 and the reciprocals'
+// product is still finite.
+__device__ __forceinline__ float2 tr_phi2(float2 g, float2& e) {
+    const float2 x = tr_mul2(make_float2(fminf(fabsf(g.x), 0x1p40f), fminf(fabsf(g.y), 0x1p40f)), tr_both(0.70710678118654752f));
+    const float2 t = tr_rcp2(tr_mad2(tr_both(0.3275911f), x, tr_both(1.0f)));
+    float2 p = tr_mad2(tr_both(1.061405429f), t, tr_both(-1.453152027f));
+    p = tr_mad2(p, t, tr_both(1.421413741f));
+    p = tr_mad2(p, t, tr_both(-0.284496736f));
+    p = tr_mad2(p, t, tr_both(0.254829592f));
+    const float2 y = tr_mul2(tr_mul2(x, tr_both(-kLog2e)), x);
+    e = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+    const float2 half = tr_mul2(tr_mul2(tr_mul2(p, t), tr_both(0.5f)), e);  // Phi(-|g|)
+    // 1 - Phi(-|g|) on the positive side
+    return make_float2(g.x >= 0.0f ? 1.0f - half.x : half.x, g.y >= 0.0f ? 1.0f - half.y : half.y);
 }
 
 // h = act(g) * u of a pair
@@ -137,27 +155,20 @@ __device__ __forceinline__ float2 tr_gate2(float2 g, float2 u) {
     if constexpr (ACT == EVO_ACT_SILU) {
         return tr_mul2(gu, tr_sigmoid2(g));
     } else {
-        float e;
-        return make_float2(gu.x * tr_phi(g.x, e), gu.y * tr_phi(g.y, e));
+        float2 e;
+        return tr_mul2(gu, tr_phi2(g, e));
     }
 }
 
 // h, dg and du of a pair from g, u and d = dH
 template <int ACT>
 __device__ __forceinline__ void tr_grad2(float2 g, float2 u, float2 d, float2& h, float2& dg, float2& du) {
-    float2 p, e;
-    if constexpr (ACT == EVO_ACT_SILU) {
-        p = tr_sigmoid2(g);
-    } else {
-        p.x = tr_phi(g.x, e.x);
-        p.y = tr_phi(g.y, e.y);
-    }
+    float2 p, e, da;
+    if constexpr (ACT == EVO_ACT_SILU) p = tr_sigmoid2(g);
+    else p = tr_phi2(g, e);
     const float2 a = tr_mul2(g, p);
-    float2 da;
-    if constexpr (ACT == EVO_ACT_SILU)
-        da = make_float2(fmaf(a.x, 1.0f - p.x, p.x), fmaf(a.y, 1.0f - p.y, p.y));
-    else
-        da = make_float2(fmaf(g.x * 0.3989422804014327f, e.x, p.x), fmaf(g.y * 0.3989422804014327f, e.y, p.y));
+    if constexpr (ACT == EVO_ACT_SILU) da = tr_mad2(a, tr_mad2(p, tr_both(-1.0f), tr_both(1.0f)), p);
+    else da = tr_mad2(tr_mul2(g, tr_both(0.3989422804014327f)), e, p);
     h = tr_mul2(a, u);
     du = tr_mul2(d, a);
     dg = tr_mul2(tr_mul2(d, u), da);
