@@ -141,6 +141,22 @@ def test_a_strip_of_rows_and_only_its_elements():
     assert torch.equal(out, whole[:, :, :, 100:120]) and (guard[buf.numel():] == 3).all()
 
 
+def test_a_tile_past_32_bit_offsets():
+    """One block's rows would hold more than 2^31 elements: few values in them, exact sums."""
+    Sq, Sk = 2100, 1 << 20
+    borders = torch.tensor([-700000, -5, 0, 5, 1000], dtype=torch.int32, device=DEV)
+    pq = torch.arange(Sq, dtype=torch.int32, device=DEV).view(1, -1)
+    pk = torch.arange(Sk, dtype=torch.int32, device=DEV).view(1, -1)
+    dpair = torch.zeros(1, 1, 1, Sq, Sk, dtype=BF16, device=DEV)
+    want = np.zeros(6)
+    for n, (i, j) in enumerate([(0, 0), (2099, Sk - 1), (2099, 3), (2048, 2047), (2080, 2084), (2070, 800000), (5, 5), (2098, 2099)]):
+        dpair[0, 0, 0, i, j] = float(n + 1)
+        want[np.searchsorted(borders.cpu().numpy(), i - j, side="right")] += n + 1
+    dtable = evo.relpos_bias_backward(dpair, borders, pq, pk)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    assert np.array_equal(_f64(dtable)[:, 0], want)
+
+
 def test_empty_sizes():
     table, borders, pq, pk, _, _, pair = make(2, 6, 8, 3, 5, FP32, seed=9)
     assert evo.relpos_bias(table, borders, pq[:, :0].contiguous(), pk).numel() == 0

@@ -70,6 +70,28 @@ def test_more_rows_than_one_chunk(waves, C, F):
     check(*make(M, C, F, BF16, seed=1), "silu", f"chunks {M}")
 
 
+@pytest.mark.parametrize("M,C,F,dt", [(19244, 16, 1200, FP32), (57100, 132, 1201, FP16), (94820, 17, 1201, BF16),
+                                      (2100000, 9, 8, FP16)], ids=str)
+def test_chunks_of_every_form(M, C, F, dt):
+    """Several chunks with fp32, and with copies of rows that are no whole 16-byte units."""
+    check(*make(M, C, F, dt, seed=M), "silu", f"chunks {M} {C} {F} {dt}")
+
+
+def test_more_row_tiles_than_a_grid_dimension():
+    """More than 65535 tiles of 128 rows, with one feature in fp32 (one chunk by bytes alone)."""
+    M = 65536 * 128 + 1000
+    x, wg, wu, wd, dy = make(M, 2, 1, FP32, seed=3)
+    y = evo.transition(x, wg, wu, wd)
+    dx, *dw = evo.transition_backward(x, wg, wu, wd, dy)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    at = torch.cat([torch.arange(0, M, 50021), torch.arange(M - 1200, M)])
+    ref, err = T.forward(x[at], wg, wu, wd, "silu", FP32)
+    within(y[at], ref, err, "y")
+    ref, err = T.backward(x, wg, wu, wd, dy, "silu", FP32)
+    for name, g, r, e in zip(("dx", "dw_gate", "dw_up", "dw_down"), (dx, *dw), ref, err):
+        within(g, r, e, name)
+
+
 @pytest.mark.parametrize("shape,dt", [((8321, 128, 512), BF16), ((8200, 40, 72), FP16), ((19100, 256, 304), BF16),
                                       ((20001, 192, 136), FP16), ((8193, 100, 130), BF16), ((38000, 64, 128), BF16),
                                       ((9000, 250, 400), FP16), ((8193, 1, 1), BF16), ((60000, 64, 64), BF16),

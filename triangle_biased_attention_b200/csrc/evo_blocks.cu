@@ -78,7 +78,8 @@ constexpr int64_t kTrWave = 148 * 128;
 
 int64_t tr_chunk_rows(int64_t M, int64_t row_bytes, bool backward) {
     const int64_t target = int64_t(backward ? 512 : 64) << 20;
-    const int64_t waves = std::max<int64_t>(1, target / (kTrWave * std::max<int64_t>(row_bytes, 1)));
+    // (and no more row tiles than a grid's y dimension, 65535, takes)
+    const int64_t waves = std::min<int64_t>(440, std::max<int64_t>(1, target / (kTrWave * std::max<int64_t>(row_bytes, 1))));
     return std::min(M, waves * kTrWave);
 }
 
@@ -822,7 +823,9 @@ RelTiles rel_bwd_tiles(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t row
     const int64_t want = std::max<int64_t>(1, 148 * std::max<int64_t>(1, held) / others);
     int64_t ti = std::max<int64_t>((Sq + want - 1) / want, 8 * per);
     ti = std::max<int64_t>(ti, (Sq + 65534) / 65535);
-    t.ti = int((ti + per - 1) / per * per);
+    ti = (ti + per - 1) / per * per;
+    // element offsets inside a tile are 32-bit (Sk < 2^29, and below 1024 unless `per` is 1)
+    t.ti = int(std::min<int64_t>(ti, kIntMax / Sk / per * per));
     t.it = (Sq + t.ti - 1) / t.ti;
     t.part_bytes = B * t.it * t.jt * H * rows * 4;
     return t;
@@ -970,8 +973,8 @@ extern "C" EVO_API int evo_relpos_bwd(const void* dpair, const int32_t* borders,
     }
     if (!dpair || (!borders && num_borders > 0) || !pos_q || !pos_k || !workspace) return EVO_ERR_INVALID_ARG;
     const RelTiles t = rel_bwd_tiles(B, Sq, Sk, H, rows);
-    // blocks of the grid's z dimension; element offsets inside a tile are 32-bit
-    if (B * H * t.chunks > 65535 || int64_t(t.ti) * Sk > kIntMax) return EVO_ERR_UNSUPPORTED_SHAPE;
+    // the grid's z and y dimensions
+    if (B * H * t.chunks > 65535 || t.it > 65535) return EVO_ERR_UNSUPPORTED_SHAPE;
     if (workspace_bytes < t.part_bytes) return EVO_ERR_INVALID_ARG;
     if (!aligned(dpair, uintptr_t(es)) || !aligned(workspace, 256)) return EVO_ERR_MISALIGNED;
     for (const int32_t* p : {borders, pos_q, pos_k, chain_q, chain_k})
