@@ -353,9 +353,9 @@ struct PadList {
         p.wp[p.n++] = int(round_up(w, 8));
     }
     bool run(int sms, cudaStream_t st) {
-        int64_t rows = 0;
-        for (int k = 0; k < p.n; ++k) rows += p.rows[k];
-        return launch_dependent(evo::evo_tr_pad_kernel, dim3(unsigned(std::min<int64_t>((rows + 7) / 8, int64_t(sms) * 8))), 256, 0, st, p);
+        int64_t runs = 0;  // of 32 16-byte units, a warp's work
+        for (int k = 0; k < p.n; ++k) runs += int64_t(p.rows[k]) * ((p.wp[k] + 255) / 256);
+        return launch_dependent(evo::evo_tr_pad_kernel, dim3(unsigned(std::min<int64_t>((runs + 7) / 8, int64_t(sms) * 8))), 256, 0, st, p);
     }
 };
 
@@ -553,17 +553,26 @@ int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
         if (L.pad && !pad_chunk(L, ws, &s, &x, &dy, p.rows, m == 0, C, F, sms, st)) return EVO_ERR_CUDA;
         char *h = ws + L.h, *dg = ws + L.dg, *du = ws + L.du;
         evo::TrMaps grad, out, wgt;
+        std::memset(&grad, 0, sizeof(grad));
         std::memset(&out, 0, sizeof(out));
         std::memset(&wgt, 0, sizeof(wgt));
-        if (!encode_rows(&grad.m[0], x, p.rows, C, s.ldc, 128, F16) || !encode_rows(&grad.m[1], s.wg, F, C, s.ldc, 128, F16) ||
-            !encode_rows(&grad.m[2], s.wu, F, C, s.ldc, 128, F16) || !encode_rows(&grad.m[3], dy, p.rows, C, s.ldc, 128, F16) ||
-            !encode_rows(&grad.m[4], s.wd, C, F, s.ldf, 64, F16) || !encode_rows(&grad.m[5], h, p.rows, ldf, ldf, 32, F16, 32) ||
-            !encode_rows(&grad.m[6], dg, p.rows, ldf, ldf, 32, F16, 32) || !encode_rows(&grad.m[7], du, p.rows, ldf, ldf, 32, F16, 32) ||
-            !encode_rows(&out.m[0], dg, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[1], s.wg, F, C, s.ldc, 64, F16) ||
-            !encode_rows(&out.m[2], du, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[3], s.wu, F, C, s.ldc, 64, F16) ||
-            !encode_rows(&wgt.m[0], x, p.rows, C, s.ldc, 64, F16) || !encode_rows(&wgt.m[1], dy, p.rows, C, s.ldc, 64, F16) ||
-            !encode_rows(&wgt.m[2], dg, p.rows, ldf, ldf, 64, F16) || !encode_rows(&wgt.m[3], du, p.rows, ldf, ldf, 64, F16) ||
-            !encode_rows(&wgt.m[4], h, p.rows, ldf, ldf, 64, F16))
+        if (!encode_rows(&grad.m[0], x, p.rows, C, s.ldc, 128, F16) || !encode_rows(&grad.m[3], dy, p.rows, C, s.ldc, 128, F16) ||
+            !encode_rows(&grad.m[4], s.wd, C, F, s.ldf, 64, F16))
+            return EVO_ERR_CUDA;
+        if (!L.gradw &&
+            (!encode_rows(&grad.m[1], s.wg, F, C, s.ldc, 128, F16) || !encode_rows(&grad.m[2], s.wu, F, C, s.ldc, 128, F16) ||
+             !encode_rows(&grad.m[5], h, p.rows, ldf, ldf, 32, F16, 32) || !encode_rows(&grad.m[6], dg, p.rows, ldf, ldf, 32, F16, 32) ||
+             !encode_rows(&grad.m[7], du, p.rows, ldf, ldf, 32, F16, 32)))
+            return EVO_ERR_CUDA;
+        if ((L.gradw || dX) &&
+            (!encode_rows(&out.m[1], s.wg, F, C, s.ldc, 64, F16) || !encode_rows(&out.m[3], s.wu, F, C, s.ldc, 64, F16)))
+            return EVO_ERR_CUDA;
+        if (dX && (!encode_rows(&out.m[0], dg, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[2], du, p.rows, ldf, ldf, 128, F16)))
+            return EVO_ERR_CUDA;
+        if (!L.gradw && p.num_which > 0 &&
+            (!encode_rows(&wgt.m[0], x, p.rows, C, s.ldc, 64, F16) || !encode_rows(&wgt.m[1], dy, p.rows, C, s.ldc, 64, F16) ||
+             !encode_rows(&wgt.m[2], dg, p.rows, ldf, ldf, 64, F16) || !encode_rows(&wgt.m[3], du, p.rows, ldf, ldf, 64, F16) ||
+             !encode_rows(&wgt.m[4], h, p.rows, ldf, ldf, 64, F16)))
             return EVO_ERR_CUDA;
         for (int w = 0; w < 3; ++w) {
             const int64_t R = w == 2 ? C : F, N = w == 2 ? F : C;

@@ -1222,9 +1222,12 @@ __global__ void __launch_bounds__(256) evo_tr_gradw_reduce_kernel(const float* _
     tr_store(out + (which == 2 ? size_t(c) * F + f : size_t(f) * C + c), s);
 }
 
-// Rows of `w` elements copied to rows of `wp` (w rounded up to 8), for up to five
-// matrices at once, a warp a row: TMA reads rows of whole 16-byte units only.
-// What lies behind column w is never read.
+// Rows of `w` elements copied to rows of `wp` (w rounded up to 8; zeros behind
+// column w), for up to five matrices at once: TMA reads rows of whole 16-byte
+// units only.  A lane forms one 16-byte unit, from 4-byte loads where the source
+// has them on such boundaries, all in flight at once (a warp a row, an element a
+// lane at a time, waited for memory 13 times a row: 22.8 us for the copies of 1733 x
+// 388 with 1555 features, 5.5 so).
 struct TrPads {
     const uint16_t* src[5];
     uint16_t* dst[5];
@@ -1236,19 +1239,29 @@ static __global__ void __launch_bounds__(256) evo_tr_pad_kernel(const TrPads p) 
     ptx::pdl_launch();
     ptx::pdl_wait();
     const int lane = threadIdx.x & 31;
-    int k = 0;
-    long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const long long step = ((long long)gridDim.x * blockDim.x) >> 5;
-    while (k < p.n) {
-        if (r >= p.rows[k]) {
-            r -= p.rows[k++];
-            continue;
+    long long t = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;  // a warp's run of 32 units
+    for (int k = 0; k < p.n; ++k) {
+        const int w = p.w[k], runs = (p.wp[k] + 255) / 256;
+        const long long all = (long long)p.rows[k] * runs;
+        const bool words = w % 2 == 0 && (reinterpret_cast<uintptr_t>(p.src[k]) & 3) == 0;
+        for (; t < all; t += step) {
+            const long long r = all <= 0x7fffffff ? int(t) / runs : t / runs;
+            const int c = (int(t - r * runs) * 32 + lane) * 8, n = w - c;
+            if (n <= 0) continue;
+            const uint16_t* x = p.src[k] + r * w + c;
+            uint32_t v[4];
+            if (words) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = 2 * e < n ? *reinterpret_cast<const uint32_t*>(x + 2 * e) : 0u;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = (2 * e < n ? uint32_t(x[2 * e]) : 0u) | (2 * e + 1 < n ? uint32_t(x[2 * e + 1]) << 16 : 0u);
+            }
+            *reinterpret_cast<uint4*>(p.dst[k] + r * p.wp[k] + c) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        const uint16_t* x = p.src[k] + r * p.w[k];
-        uint16_t* y = p.dst[k] + r * p.wp[k];
-#pragma unroll 4
-        for (int c = lane; c < p.w[k]; c += 32) y[c] = x[c];
-        r += step;
+        t -= all;
     }
 }
 
