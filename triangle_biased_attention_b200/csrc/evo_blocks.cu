@@ -387,19 +387,27 @@ bool tma_rows(const void* p, int64_t C) { return C % 8 == 0 && aligned(p, 16); }
 
 int tiles_of(int64_t n, int64_t tile) { return int((n + tile - 1) / tile); }
 
-// Y or dX of one chunk: 256 channels a tile where there are more than 128 and
-// tiles enough for the SMs.
+// Channels of a tile of Y or dX: 256 where there are more than 128 and tiles
+// enough for the SMs, 64 where tiles of 128 would leave half of the SMs idle.
+int out_width(int rows, int64_t C, int sms) {
+    const int tiles = tiles_of(rows, 128) * tiles_of(C, 128);
+    return C > 128 && tiles > sms ? 256 : 2 * tiles <= sms ? 64 : 128;
+}
+
+// Y or dX of one chunk.
 template <int KIND, bool F16>
 int launch_out(int dev, int sms, evo::TrMaps& maps, evo::TrMmaParams p, void* out, cudaStream_t st) {
     p.out = static_cast<uint16_t*>(out);
     p.tma_out = tma_rows(out, p.C);
     if (p.tma_out && !encode_rows(&maps.m[KIND == evo::TR_OUT ? 2 : 4], out, p.rows, p.C, p.C, 32, F16, 32)) return EVO_ERR_CUDA;
+    const int width = out_width(p.rows, p.C, sms);
     p.tiles_m = tiles_of(p.rows, 128);
-    const bool wide = p.C > 128 && p.tiles_m * tiles_of(p.C, 128) > sms;
-    p.tiles_n = tiles_of(p.C, wide ? 256 : 128);
+    p.tiles_n = tiles_of(p.C, width);
     p.num_tiles = p.tiles_m * p.tiles_n;
     p.kb = tiles_of(p.F, 64);
-    return wide ? launch_mma<KIND, 0, F16, 256>(dev, sms, maps, p, st) : launch_mma<KIND, 0, F16, 128>(dev, sms, maps, p, st);
+    return width == 256   ? launch_mma<KIND, 0, F16, 256>(dev, sms, maps, p, st)
+           : width == 128 ? launch_mma<KIND, 0, F16, 128>(dev, sms, maps, p, st)
+                          : launch_mma<KIND, 0, F16, 64>(dev, sms, maps, p, st);
 }
 
 template <int ACT, bool F16, int CN>
@@ -458,7 +466,7 @@ int run_fwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
         if (!encode_rows(&gate.m[0], x, p.rows, C, s.ldc, 128, F16) || !encode_rows(&gate.m[1], s.wg, F, C, s.ldc, 128, F16) ||
             !encode_rows(&gate.m[2], s.wu, F, C, s.ldc, 128, F16) ||
             !encode_rows(&gate.m[3], ws + L.h, p.rows, ldf, ldf, 32, F16, 32) ||
-            !encode_rows(&out.m[0], ws + L.h, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[1], s.wd, C, F, s.ldf, 128, F16))
+            !encode_rows(&out.m[0], ws + L.h, p.rows, ldf, ldf, 128, F16) || !encode_rows(&out.m[1], s.wd, C, F, s.ldf, out_width(p.rows, C, sms) == 64 ? 64 : 128, F16))
             return EVO_ERR_CUDA;
         p.tiles_m = tiles_of(p.rows, 128);
         p.tiles_n = tiles_of(F, 128);

@@ -67,7 +67,7 @@ struct TrMmaParams {
 template <int KIND, int BN, bool F16>
 struct TrCfg {
     static constexpr int THREADS = 384;
-    static constexpr int STAGES = KIND == TR_GRAD ? 3 : 4;
+    static constexpr int STAGES = KIND == TR_GRAD ? 3 : BN == 64 ? 6 : 4;
     static constexpr int BOXES = KIND == TR_GRAD ? 6144 : 4096;  // a warp's boxes for its results
     static constexpr int OPER_A = 128 * 128;   // 128 rows x 64 k, or 64 k x 128 columns
     static constexpr int OPER_B = BN * 128;
@@ -328,9 +328,10 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     } else if constexpr (KIND == TR_OUT) {
                         ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
                         ptx::tma_load_2d(a, &maps.m[0], f, k, 128 * tm);
+                        constexpr int R = BN < 128 ? 64 : 128;  // rows of Wd's box
 #pragma unroll
-                        for (int x = 0; x < BN / 128; ++x)
-                            ptx::tma_load_2d(b + 16384 * x, &maps.m[1], f, k, BN * tn + 128 * x);
+                        for (int x = 0; x < BN / R; ++x)
+                            ptx::tma_load_2d(b + R * 128 * x, &maps.m[1], f, k, BN * tn + R * x);
                     } else if constexpr (KIND == TR_DX) {
                         ptx::mbar_arrive_expect_tx(f, C::STAGE_BYTES);
                         ptx::tma_load_2d(a, &maps.m[second ? 2 : 0], f, k, 128 * tm);
