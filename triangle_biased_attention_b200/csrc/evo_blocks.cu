@@ -162,10 +162,15 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
             L->splits = std::max<int64_t>(1, std::min(148 / ((F + 63) / 64), (L->chunk + 127) / 128));
             L->part = take(3 * L->splits * C * round_up(F, 64) * 4);
         } else {
-            // as many ranges as keep the tiles within one wave of 148 SMs, none under 512 rows
+            // as many ranges as keep the tiles within one wave of 148 SMs, none under 512
+            // rows; one range, without slots, where the rows are few beside the weights,
+            // so that the slots cost more than the shorter sums save. Whole backward with
+            // one range against 512-row ones, us: C = 256, F = 512: 1024 rows 22.4 / 24.3,
+            // 2048 28.8 / 25.6; C = 256, F = 1024: 2048 rows 32.7 / 39.3, 4096 48.9 / 44.4;
+            // C = 384, F = 1536: 1024 rows 30.3 / 50.8, 4096 76.1 / 76.0
             const int64_t bn = C > 128 ? 256 : 128;
             const int64_t tiles = 2 * ((F + 127) / 128) * ((C + bn - 1) / bn) + ((C + 127) / 128) * ((F + 255) / 256);
-            L->splits = std::max<int64_t>(1, std::min(148 / tiles, (L->chunk + 511) / 512));
+            L->splits = !L->pad && L->chunk * 128 <= fc ? 1 : std::max<int64_t>(1, std::min(148 / tiles, (L->chunk + 511) / 512));
             L->split_rows = round_up((L->chunk + L->splits - 1) / L->splits, 64);
             L->direct = L->splits == 1 && L->chunk == M && !L->pad;
             if (!L->direct) {
