@@ -80,7 +80,7 @@ struct RelLookup {
 };
 
 // Fills the block's shared copies; every thread of the block calls it.
-__device__ __forceinline__ RelLookup rel_setup(const int* __restrict__ borders, int nb, int* sborders, uint16_t* lut) {
+__device__ __forceinline__ RelLookup rel_setup(const int* borders, int nb, int* sborders, uint16_t* lut) {
     for (int i = threadIdx.x; i < nb; i += blockDim.x) sborders[i] = borders[i];
     __syncthreads();
     RelLookup L;
@@ -141,7 +141,7 @@ __device__ __forceinline__ uint32_t rel_add(uint32_t a, uint32_t b) {
 // group.  VEC: a thread's columns are 16 whole bytes of each head's row of P,
 // written at once (the values of its columns are transposed in registers); else
 // its columns lie the block's width apart and are written one by one.
-// 2048 x 2048 x 8 heads, bf16, with a base: 32.6 us, 134 MB, 4.1 TB/s (L2 takes part of
+// 2048 x 2048 x 8 heads, bf16, with a base: 30.9 us, 134 MB, 4.35 TB/s (L2 takes part of
 // the writes); one shared-memory read for all heads instead of one each, and 16-byte
 // writes, brought it from 254 us.  The loads and stores in flight are the limit
 // now (issue 39 %).
@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const Re
     constexpr int HEADS = NW * 4 / int(sizeof(T));
     constexpr int COLS = VEC ? 16 / int(sizeof(T)) : kRelCols;
     extern __shared__ __align__(16) uint8_t rel_sm[];
+    ptx::pdl_launch();
+    ptx::pdl_wait();
     T* stable = reinterpret_cast<T*>(rel_sm);
     int* sborders = reinterpret_cast<int*>(rel_sm + (p.rows * NW * 4 + 15) / 16 * 16);
     uint16_t* lut = reinterpret_cast<uint16_t*>(sborders + (p.nb + 3) / 4 * 4);
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const Re
 // beside the memory, so the distance table holds the bins' byte offsets (a row of
 // another range of bins: the one behind the last, which nobody reads) and the
 // positions are kept as byte offsets into it: an element costs a subtraction, a
-// clamp, a read and an addition.  1733 x 1733 x 16 heads, fp32: 69 us, 192 MB, 2.8 TB/s, the
+// clamp, a read and an addition.  1733 x 1733 x 16 heads, fp32: 67 us, 192 MB, 2.85 TB/s, the
 // issue slots 67 % busy (an odd row length allows 4-byte loads only, and log-spaced
 // buckets move some column of a warp in most rows).  That needs positions below 2^27 in size and
 // borders within the table's span; other blocks search the borders.
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     uint32_t* lut = reinterpret_cast<uint32_t*>(sborders + (p.nb + 3) / 4 * 4);
     for (int i = threadIdx.x; i < (nbins + 1) * (kRelBwdThreads / 4); i += kRelBwdThreads)
         reinterpret_cast<float4*>(bins)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    ptx::pdl_launch();
     for (int i = threadIdx.x; i < p.nb; i += kRelBwdThreads) sborders[i] = p.borders[i];
 
     const int lanes = 1 << p.lane_cols, tx = threadIdx.x & (lanes - 1), ty = threadIdx.x >> p.lane_cols;
@@ -388,10 +391,14 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     }
 }
 
-// dtable[r, h] = the sum over the tiles, a warp an element, in a fixed order.
+// dtable[r, h] = the sum over the tiles, a warp an element, in a fixed order.  (No
+// restrict pointers where a kernel waits for the one before: a read could move
+// ahead of the wait.)
 template <typename T>
-__global__ void __launch_bounds__(256) evo_relpos_bwd_sum_kernel(const float* __restrict__ part, long long tiles, int H,
-                                                                 int rows, T* __restrict__ dtable) {
+__global__ void __launch_bounds__(256) evo_relpos_bwd_sum_kernel(const float* part, long long tiles, int H,
+                                                                 int rows, T* dtable) {
+    ptx::pdl_launch();
+    ptx::pdl_wait();
     const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (w >= (long long)H * rows) return;

@@ -1217,7 +1217,7 @@ evo_tr_gradw_kernel(const __grid_constant__ TrMaps maps, const TrGradwParams p) 
 // The weight gradients from the shares' sums, added in order and rounded to the
 // type, a thread an element: [3][splits][C][ldp], the first two turned into [F, C].
 template <typename T>
-__global__ void __launch_bounds__(256) evo_tr_gradw_reduce_kernel(const float* __restrict__ part, int splits, int C, int F, int ldp,
+__global__ void __launch_bounds__(256) evo_tr_gradw_reduce_kernel(const float* part, int splits, int C, int F, int ldp,
                                                                   T* dwg, T* dwu, T* dwd) {
     ptx::pdl_launch();
     ptx::pdl_wait();
