@@ -70,6 +70,12 @@ def test_more_rows_than_one_chunk(waves, C, F):
     check(*make(M, C, F, BF16, seed=1), "silu", f"chunks {M}")
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("shape", [(100, 128, 512), (509, 96, 130), (3000, 35, 130), (1300, 101, 397), (2000, 128, 512)], ids=str)
+def test_fp32_rows_in_groups_and_in_tiles(shape, act):
+    check(*make(*shape, FP32, seed=shape[0]), act, f"{shape} {act}")
+
+
 @pytest.mark.parametrize("M,C,F,dt", [(19244, 16, 1200, FP32), (57100, 132, 1201, FP16), (94820, 17, 1201, BF16),
                                       (2100000, 9, 8, FP16)], ids=str)
 def test_chunks_of_every_form(M, C, F, dt):

@@ -99,9 +99,15 @@ struct TrLayout {
     int64_t total = 0;
 };
 
-// The form for a few rows reads X and H from shared memory.
-bool tr_few(int64_t M, int64_t C, int64_t F) {
-    return M <= evo::kTrFewRows && 8 * C * 4 <= evo::kTrFewBytes && 8 * F * 4 <= evo::kTrFewBytes;
+// The form for a few rows reads X and H from shared memory, in groups of 8 rows;
+// 16-bit rows past 8 are faster on the tensor cores. With fp32 its time grows with
+// M C F, while the tiles' is that of one tile's walk over C and F until the rows
+// fill the SMs. Measured, us, groups against tiles: C = 128, F = 512: 16 rows 9.5 / 49.5,
+// 256 29 / 55; C = 384, F = 1536: 64 rows 52 / 143, 192 135 / 155, 256 178 / 155; C = 464, F =
+// 1856: 128 rows 163 / 185, 192 237 / 188; C = 1024, F = 4096: 32 rows 188 / 377, 96 548 / 399.
+bool tr_few(int64_t M, int64_t C, int64_t F, int dtype) {
+    if (8 * C * 4 > evo::kTrFewBytes || 8 * F * 4 > evo::kTrFewBytes) return false;
+    return M <= evo::kTrFewRows || (dtype == EVO_DTYPE_FP32 && M * C * F <= 50000 * (C + F));
 }
 
 // The one-kernel forward holds Y of 128 rows in tensor memory (C <= 256) and
@@ -128,7 +134,7 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
     const int64_t es = elem_bytes(dtype);
     // C, F <= 2^20 and M < 2^31 (check_transition): the products below fit
     const int64_t fc = F * C;
-    if (!backward && tr_few(M, C, F)) {
+    if (!backward && tr_few(M, C, F, dtype)) {
         L->few = true;
         L->chunk = M;
         L->total = round_up(M * F * 4, 256);
@@ -646,9 +652,9 @@ int run_few(int dev, const evo::TrFewParams<T>& p, bool vec, cudaStream_t st) {
     if (!attr[0][vec].ensure(dev, gate, evo::kTrFewBytes) || !attr[1][vec].ensure(dev, out, evo::kTrFewBytes))
         return EVO_ERR_CUDA;
     const unsigned blocks = std::min(blocks_of(p.F, 8), 148u * 8);
-    const unsigned channels = blocks_of(p.C, 8 / p.split);
-    return launch_dependent(gate, dim3(blocks), evo::kTrFewThreads, MB * p.C * 4, st, p) &&
-                   launch_dependent(out, dim3(channels), evo::kTrFewThreads, MB * p.F * 4, st, p)
+    const unsigned channels = blocks_of(p.C, 8 / p.split), groups = blocks_of(p.M, MB);
+    return launch_dependent(gate, dim3(blocks, groups), evo::kTrFewThreads, MB * p.C * 4, st, p) &&
+                   launch_dependent(out, dim3(channels, groups), evo::kTrFewThreads, MB * p.F * 4, st, p)
                ? EVO_OK
                : EVO_ERR_CUDA;
 }

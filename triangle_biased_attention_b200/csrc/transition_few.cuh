@@ -1,6 +1,6 @@
-// The transition forward for a few rows (one token and up): bound by reading the
-// weights once, so the work is spread by weight rows over every SM instead of by
-// row tiles.  Two kernels: H, a warp a feature (both projections, the activation
+// The transition forward for a few rows (one token and up), in groups of at most 8:
+// bound by reading the weights, so the work is spread by weight rows over every SM
+// instead of by row tiles.  Two kernels: H, a warp a feature (both projections, the activation
 // and the product), then Y, one to eight warps a channel.  X and H lie in shared
 // memory in fp32: nothing is rounded before Y.  The second kernel starts beside the
 // first (programmatic dependent launch) and has its first weights on their way
@@ -14,7 +14,7 @@
 namespace evo {
 
 constexpr int kTrFewThreads = 256;
-constexpr int kTrFewRows = 8;              // most rows
+constexpr int kTrFewRows = 8;              // most rows of a group (grid y: groups)
 constexpr int kTrFewBytes = 128 * 1024;    // most bytes of X or H in shared memory
 
 template <typename T>
@@ -53,7 +53,10 @@ __global__ void __launch_bounds__(kTrFewThreads) evo_tr_few_gate_kernel(const Tr
     // may start only once every kernel before this one has ended
     ptx::pdl_wait();
     ptx::pdl_launch();
-    for (int i = threadIdx.x; i < MB * p.C; i += kTrFewThreads) few_smem[i] = i < p.M * p.C ? tr_f32(p.x[i]) : 0.0f;
+    const int m0 = blockIdx.y * MB, M = min(MB, p.M - m0);
+    const T* x = p.x + (long long)m0 * p.C;
+    float* h = p.h + (long long)m0 * p.F;
+    for (int i = threadIdx.x; i < MB * p.C; i += kTrFewThreads) few_smem[i] = i < M * p.C ? tr_f32(x[i]) : 0.0f;
     __syncthreads();
     const int lane = threadIdx.x & 31;
     for (int f = (blockIdx.x * kTrFewThreads + threadIdx.x) >> 5; f < p.F; f += gridDim.x * (kTrFewThreads / 32)) {
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(kTrFewThreads) evo_tr_few_gate_kernel(const Tr
                 g[m] += __shfl_xor_sync(0xffffffffu, g[m], o);
                 u[m] += __shfl_xor_sync(0xffffffffu, u[m], o);
             }
-            if (lane == m && m < p.M) p.h[(long long)m * p.F + f] = tr_act<ACT>(g[m]) * u[m];
+            if (lane == m && m < M) h[(long long)m * p.F + f] = tr_act<ACT>(g[m]) * u[m];
         }
     }
 }
@@ -98,7 +101,10 @@ __global__ void __launch_bounds__(kTrFewThreads) evo_tr_few_out_kernel(const TrF
     ptx::pdl_launch();
     if (f < p.F) tr_few_load<T, VE>(wd + f, w);  // no result of the kernel before
     ptx::pdl_wait();
-    for (int i = threadIdx.x; i < MB * p.F; i += kTrFewThreads) few_smem[i] = i < p.M * p.F ? p.h[i] : 0.0f;
+    const int m0 = blockIdx.y * MB, M = min(MB, p.M - m0);
+    const float* h = p.h + (long long)m0 * p.F;
+    T* out = p.y + (long long)m0 * p.C;
+    for (int i = threadIdx.x; i < MB * p.F; i += kTrFewThreads) few_smem[i] = i < M * p.F ? h[i] : 0.0f;
     __syncthreads();
     float y[MB] = {};
     while (f < p.F) {
@@ -123,9 +129,9 @@ __global__ void __launch_bounds__(kTrFewThreads) evo_tr_few_out_kernel(const TrF
         const int k = threadIdx.x / MB, m = threadIdx.x % MB, ck = blockIdx.x * per + k;
         float s = 0.0f;
         for (int i = 0; i < p.split; ++i) s += part[k * p.split + i][m];
-        if (ck < p.C && m < p.M) {
-            if constexpr (sizeof(T) == 4) p.y[(long long)m * p.C + ck] = s;
-            else tr_store(p.y + (long long)m * p.C + ck, s);
+        if (ck < p.C && m < M) {
+            if constexpr (sizeof(T) == 4) out[(long long)m * p.C + ck] = s;
+            else tr_store(out + (long long)m * p.C + ck, s);
         }
     }
 }
