@@ -99,15 +99,20 @@ struct TrLayout {
     int64_t total = 0;
 };
 
-// The form for a few rows reads X and H from shared memory, in groups of 8 rows;
-// 16-bit rows past 8 are faster on the tensor cores. With fp32 its time grows with
+// The form for a few rows reads X and H from shared memory, in groups of 8 rows.
+// 16-bit, us, against the tensor cores: one row 2.9 / 5.3 (C = 64, F = 256) to 11.3 / 20.5
+// (1024, 4096); 4 rows 5.1 / 7.1 (128, 512), 11.1 / 9.2 (256, 1024); 8 rows 7.5 / 7.1 (128, 512);
+// where rows would have to be copied for TMA first, 8 rows 8.3 / 9.5 (100, 397), 14.9 / 16.7
+// (388, 1555). With fp32 its time grows with
 // M C F, while the tiles' is that of one tile's walk over C and F until the rows
 // fill the SMs. Measured, us, groups against tiles: C = 128, F = 512: 16 rows 9.5 / 49.5,
 // 256 29 / 55; C = 384, F = 1536: 64 rows 52 / 143, 192 135 / 155, 256 178 / 155; C = 464, F =
 // 1856: 128 rows 163 / 185, 192 237 / 188; C = 1024, F = 4096: 32 rows 188 / 377, 96 548 / 399.
 bool tr_few(int64_t M, int64_t C, int64_t F, int dtype) {
     if (8 * C * 4 > evo::kTrFewBytes || 8 * F * 4 > evo::kTrFewBytes) return false;
-    return M <= evo::kTrFewRows || (dtype == EVO_DTYPE_FP32 && M * C * F <= 50000 * (C + F));
+    if (dtype == EVO_DTYPE_FP32) return M <= evo::kTrFewRows || M * C * F <= 50000 * (C + F);
+    if (C % 8 == 0 && F % 8 == 0) return M == 1 || (M <= 4 && C * F <= 100000);
+    return M == 1 || (M <= evo::kTrFewRows && C * F <= 700000);
 }
 
 // The one-kernel forward holds Y of 128 rows in tensor memory (C <= 256) and
@@ -646,8 +651,9 @@ int run_bwd_mma(int dev, const void* X, const void* Wg, const void* Wu, const vo
 template <typename T, int ACT, int MB>
 int run_few(int dev, const evo::TrFewParams<T>& p, bool vec, cudaStream_t st) {
     constexpr int VE = 16 / int(sizeof(T));
-    auto gate = vec ? evo::evo_tr_few_gate_kernel<T, ACT, MB, VE> : evo::evo_tr_few_gate_kernel<T, ACT, MB, 1>;
-    auto out = vec ? evo::evo_tr_few_out_kernel<T, MB, VE> : evo::evo_tr_few_out_kernel<T, MB, 1>;
+    constexpr int WIDE = MB == 8 && sizeof(T) == 2 ? 1 : VE;  // (tr_few: no whole 16-byte units there)
+    auto gate = vec ? evo::evo_tr_few_gate_kernel<T, ACT, MB, WIDE> : evo::evo_tr_few_gate_kernel<T, ACT, MB, 1>;
+    auto out = vec ? evo::evo_tr_few_out_kernel<T, MB, WIDE> : evo::evo_tr_few_out_kernel<T, MB, 1>;
     static AttrOnce attr[2][2];
     if (!attr[0][vec].ensure(dev, gate, evo::kTrFewBytes) || !attr[1][vec].ensure(dev, out, evo::kTrFewBytes))
         return EVO_ERR_CUDA;
