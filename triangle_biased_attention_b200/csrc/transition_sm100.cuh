@@ -40,6 +40,7 @@
 
 #include <cuda.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "tile_sm100.cuh"
 #include "transition_common.cuh"
@@ -128,21 +129,55 @@ __device__ __forceinline__ float2 tr_rcp2(float2 a) {
 
 // sigmoid of two elements.  One reciprocal serves both: 1/a = b / (a b), which
 // leaves the special-function unit 1.5 instructions an element instead of 2.
-// The exponent is held at 2^60 so that a b stays finite: below g = -41 the
-// result is 2^-60 instead of e^g, both nothing beside the rounding of g u.
+// FAR false: |g| <= kTrNear, so that a b is finite.  FAR true, any g: from
+// e^-|g| <= 1, as 1 / (1 + e^-|g|) on the positive side and e^-|g| times that on
+// the negative one, which goes to 0 with e^g (below g = -87 it is 0).
+template <bool FAR>
 __device__ __forceinline__ float2 tr_sigmoid2(float2 g) {
-    const float2 x = tr_mul2(g, make_float2(-kLog2e, -kLog2e));
-    const float2 e = make_float2(ptx::ex2_approx(fminf(x.x, 60.0f)), ptx::ex2_approx(fminf(x.y, 60.0f)));
-    return tr_rcp2(tr_add2(e, tr_both(1.0f)));
+    float2 x = tr_mul2(g, make_float2(-kLog2e, -kLog2e));
+    if constexpr (FAR) x = make_float2(fminf(-fabsf(x.x), 0.0f), fminf(-fabsf(x.y), 0.0f));  // (NaN: 0, so that it stays its own)
+    const float2 e = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
+    const float2 s = tr_rcp2(tr_add2(e, tr_both(1.0f)));
+    return FAR ? tr_mul2(s, make_float2(g.x < 0.0f ? e.x : 1.0f, g.y < 0.0f ? e.y : 1.0f)) : s;
+}
+
+// Gates up to this size on either side take the short forms: (1 + e^43)^2 < 2^126,
+// within the range of the reciprocal that serves two elements.
+constexpr float kTrNear = 43.0f;
+
+// Whether all of a lane's gates are near (false with a NaN among them).  One
+// comparison a gate, as holding each exponent back by itself would cost.
+template <int N>
+__device__ __forceinline__ bool tr_near(const float (&g)[N]) {
+    float m[4] = {};
+#pragma unroll
+    for (int e = 0; e < N; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m[e & 3]) : "f"(fabsf(g[e])));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m[0]) : "f"(m[1]));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m[2]) : "f"(m[3]));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m[0]) : "f"(m[2]));
+    return m[0] <= kTrNear;
+}
+
+// A gate as a factor of its sigmoid or Phi: finite, so that a sum G that has
+// overflowed gives act's limits, 0 and (rounded) infinity, and not 0 times infinity.
+__device__ __forceinline__ float2 tr_finite2(float2 g) {
+    const float big = 3.402823466e38f;
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(g.x) : "f"(big));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(g.y) : "f"(big));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.x) : "f"(-big));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.y) : "f"(-big));
+    return g;
 }
 
 // Phi(g) and e^(-g^2/2) of two elements: the complementary error function by
 // Abramowitz and Stegun's formula 7.1.26 (absolute error at most 1.5e-7, below the
 // rounding of a 16-bit result and of the same size as the fp32 error of g itself).
-// |g| is held at 2^40, where the exponential has long been 0 and the reciprocals'
-// product is still finite.
+// FAR (not all gates near): |g| is held at 2^40, where the exponential has long
+// been 0 and the reciprocals' product is still finite.
+template <bool FAR>
 __device__ __forceinline__ float2 tr_phi2(float2 g, float2& e) {
-    const float2 x = tr_mul2(make_float2(fminf(fabsf(g.x), 0x1p40f), fminf(fabsf(g.y), 0x1p40f)), tr_both(0.70710678118654752f));
+    const float2 a = make_float2(fabsf(g.x), fabsf(g.y));
+    const float2 x = tr_mul2(FAR ? make_float2(fminf(a.x, 0x1p40f), fminf(a.y, 0x1p40f)) : a, tr_both(0.70710678118654752f));
     const float2 t = tr_rcp2(tr_mad2(tr_both(0.3275911f), x, tr_both(1.0f)));
     float2 p = tr_mad2(tr_both(1.061405429f), t, tr_both(-1.453152027f));
     p = tr_mad2(p, t, tr_both(1.421413741f));
@@ -155,30 +190,61 @@ __device__ __forceinline__ float2 tr_phi2(float2 g, float2& e) {
     return make_float2(g.x >= 0.0f ? 1.0f - half.x : half.x, g.y >= 0.0f ? 1.0f - half.y : half.y);
 }
 
-// h = act(g) * u of a pair
-template <int ACT>
+// h = act(g) * u of a pair.  (act(g) first: g u may overflow where act(g) is 0.)
+template <int ACT, bool FAR>
 __device__ __forceinline__ float2 tr_gate2(float2 g, float2 u) {
-    const float2 gu = tr_mul2(g, u);
-    if constexpr (ACT == EVO_ACT_SILU) {
-        return tr_mul2(gu, tr_sigmoid2(g));
-    } else {
-        float2 e;
-        return tr_mul2(gu, tr_phi2(g, e));
-    }
+    float2 p, e;
+    if constexpr (ACT == EVO_ACT_SILU) p = tr_sigmoid2<FAR>(g);
+    else p = tr_phi2<FAR>(g, e);
+    return tr_mul2(tr_mul2(FAR ? tr_finite2(g) : g, p), u);
 }
 
 // h, dg and du of a pair from g, u and d = dH
-template <int ACT>
+template <int ACT, bool FAR>
 __device__ __forceinline__ void tr_grad2(float2 g, float2 u, float2 d, float2& h, float2& dg, float2& du) {
     float2 p, e, da;
-    if constexpr (ACT == EVO_ACT_SILU) p = tr_sigmoid2(g);
-    else p = tr_phi2(g, e);
+    if constexpr (ACT == EVO_ACT_SILU) p = tr_sigmoid2<FAR>(g);
+    else p = tr_phi2<FAR>(g, e);
+    if (FAR) g = tr_finite2(g);
     const float2 a = tr_mul2(g, p);
     if constexpr (ACT == EVO_ACT_SILU) da = tr_mad2(a, tr_mad2(p, tr_both(-1.0f), tr_both(1.0f)), p);
     else da = tr_mad2(tr_mul2(g, tr_both(0.3989422804014327f)), e, p);
     h = tr_mul2(a, u);
     du = tr_mul2(d, a);
-    dg = tr_mul2(tr_mul2(d, u), da);
+    dg = tr_mul2(tr_mul2(u, da), d);
+}
+
+// N gates and ups of a lane: h in place of g.  A lane with a gate that is not
+// near takes the longer form for all of its own.
+template <int ACT, int N>
+__device__ __forceinline__ void tr_gate_all(float (&g)[N], const float (&u)[N]) {
+    auto all = [&](auto far) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 h = tr_gate2<ACT, decltype(far)::value>(make_float2(g[e], g[e + 1]), make_float2(u[e], u[e + 1]));
+            g[e] = h.x, g[e + 1] = h.y;
+        }
+    };
+    if (tr_near(g)) all(std::false_type{});
+    else all(std::true_type{});
+}
+
+// dg, du and h in place of g, u and d
+template <int ACT, int N>
+__device__ __forceinline__ void tr_grad_all(float (&g)[N], float (&u)[N], float (&d)[N]) {
+    auto all = [&](auto far) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            float2 h, dg, du;
+            tr_grad2<ACT, decltype(far)::value>(make_float2(g[e], g[e + 1]), make_float2(u[e], u[e + 1]),
+                                                make_float2(d[e], d[e + 1]), h, dg, du);
+            d[e] = h.x, d[e + 1] = h.y;
+            g[e] = dg.x, g[e + 1] = dg.y;
+            u[e] = du.x, u[e + 1] = du.y;
+        }
+    };
+    if (tr_near(g)) all(std::false_type{});
+    else all(std::true_type{});
 }
 
 template <bool F16>
@@ -464,13 +530,8 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     ptx::tmem_ld_wait_x32(reinterpret_cast<uint32_t*>(g));
                     ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(u));
                     if (c == 1) release();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 h = tr_gate2<ACT>(make_float2(g[2 * e], g[2 * e + 1]),
-                                                       make_float2(u[2 * e], u[2 * e + 1]));
-                        g[2 * e] = h.x;
-                        g[2 * e + 1] = h.y;
-                    }
+                    tr_gate_all<ACT>(g, u);
+                    __syncwarp();
                     put16(&maps.m[3], 128 * tn + 64 * half + 32 * c, m0, g);
                 }
             } else if constexpr (KIND == TR_GRAD) {
@@ -486,15 +547,8 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
                     ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(d));
                     ptx::reg_fence_x8(reinterpret_cast<uint32_t*>(d) + 8);
                     if (c == 3) release();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float2 h, dg, du;
-                        tr_grad2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]),
-                                      make_float2(d[2 * e], d[2 * e + 1]), h, dg, du);
-                        d[2 * e] = h.x, d[2 * e + 1] = h.y;
-                        g[2 * e] = dg.x, g[2 * e + 1] = dg.y;
-                        u[2 * e] = du.x, u[2 * e + 1] = du.y;
-                    }
+                    tr_grad_all<ACT>(g, u, d);
+                    __syncwarp();
                     if ((c & 1) == 0) {  // the boxes of the 32 features before have been read
                         ptx::bulk_wait_read<0>();
                         __syncwarp();
@@ -894,11 +948,10 @@ evo_tr_fused_kernel(const __grid_constant__ TrMaps maps, const TrFusedParams p) 
             ptx::tc_fence_before();
             ptx::mbar_arrive_elect(bar(C::GE));
             uint32_t w[16];
+            tr_gate_all<ACT>(g, u);
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float2 hv = tr_gate2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]));
-                w[e] = tr_pack<F16>(hv.x, hv.y);
-            }
+            for (int e = 0; e < 16; ++e) w[e] = tr_pack<F16>(g[2 * e], g[2 * e + 1]);
             // the product of the chunk before has read the H tile
             ok = wait_warp(bar(C::HE), uint32_t(q & 1) ^ 1u, abort_flag);
             if (!ok) break;
@@ -1139,15 +1192,8 @@ evo_tr_gradw_kernel(const __grid_constant__ TrMaps maps, const TrGradwParams p) 
             ptx::reg_fence_x32(reinterpret_cast<uint32_t*>(d));
             ptx::tc_fence_before();
             ptx::mbar_arrive_elect(bar(C::GE + b));
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float2 hv, dgv, duv;
-                tr_grad2<ACT>(make_float2(g[2 * e], g[2 * e + 1]), make_float2(u[2 * e], u[2 * e + 1]),
-                              make_float2(d[2 * e], d[2 * e + 1]), hv, dgv, duv);
-                d[2 * e] = hv.x, d[2 * e + 1] = hv.y;
-                g[2 * e] = dgv.x, g[2 * e + 1] = dgv.y;
-                u[2 * e] = duv.x, u[2 * e + 1] = duv.y;
-            }
+            tr_grad_all<ACT>(g, u, d);
+            __syncwarp();
             // the products of the tile before have read its dG, dU and H
             ok = wait_warp(bar(C::DE), uint32_t(q & 1) ^ 1u, abort_flag);
             if (!ok) break;
