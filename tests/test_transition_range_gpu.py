@@ -95,7 +95,7 @@ FORWARD = [
 
 
 @pytest.mark.parametrize("dt", [BF16, FP16], ids=lambda d: str(d)[6:])
-@pytest.mark.parametrize("act", ["silu"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("form", FORWARD, ids=str)
 def test_forward_16_bit(form, act, dt):
     C, F, step, many = form
@@ -111,7 +111,7 @@ def test_forward_16_bit(form, act, dt):
 
 
 @pytest.mark.parametrize("dt", [BF16, FP16], ids=lambda d: str(d)[6:])
-@pytest.mark.parametrize("act", ["silu"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("C,F", [(16, 16), (128, 200), (136, 16), (100, 397), (300, 100)])
 def test_backward_16_bit(C, F, act, dt):
     pairs = rows(dt)
