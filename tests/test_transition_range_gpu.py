@@ -129,6 +129,38 @@ def test_backward_16_bit(C, F, act, dt):
     within(dx[:, 1], du, edu, g, u, f"{C} {F} {act} {dt} dU")
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("form", [(16, 16, 1, 0), (16, 16, 8, 0), (50, 18, 0, 0), (130, 70, 0, 12000), (136, 24, 0, 12000)], ids=str)
+def test_forward_fp32(form, act):
+    C, F, step, many = form
+    pairs = rows(FP32, many)
+    x, wg, wu, wd = inputs(pairs, C, F, FP32)
+    step = step or x.shape[0]
+    y = torch.cat([evo.transition(x[m:m + step], wg, wu, wd, act=act) for m in range(0, x.shape[0], step)])
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    g, u = pairs[:, 0].numpy(), pairs[:, 1].numpy()
+    (h, err), _, _ = bounds(g, u, np.ones_like(g), act, FP32)
+    for c in (0, 1, min(C, F) - 1):
+        within(y[:, c], h, err, g, u, f"{form} {act} channel {c}")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("C,F,many", [(16, 16, 0), (50, 18, 0), (136, 24, 12000)])
+def test_backward_fp32(C, F, many, act):
+    pairs = rows(FP32, many)
+    x, wg, wu, wd = inputs(pairs, C, F, FP32)
+    g, u = pairs[:, 0].numpy(), pairs[:, 1].numpy()
+    n = min(C, F)
+    at, d = np.arange(len(g)) % n, np.where(np.arange(len(g)) % 2, 2.0, -0.5)
+    dy = torch.zeros(len(g), C)
+    dy[torch.arange(len(g)), torch.from_numpy(at)] = torch.from_numpy(d).float()
+    dx, *dw = evo.transition_backward(x, wg, wu, wd, dy.cuda(), act=act)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    _, (du, edu), (dg, edg) = bounds(g, u, d, act, FP32)
+    within(dx[:, 0], dg, edg, g, u, f"{C} {F} {act} dG")
+    within(dx[:, 1], du, edu, g, u, f"{C} {F} {act} dU")
+
+
 @pytest.mark.parametrize("dt", [BF16, FP16, FP32], ids=lambda d: str(d)[6:])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("C,F", [(16, 16), (136, 24), (300, 100)])
@@ -145,11 +177,12 @@ def test_weights_behind_closed_gates_have_no_gradient(C, F, act, dt):
         assert float(t.double().abs().max()) <= 2.0 ** -100, (name, float(t.double().abs().max()))
 
 
+@pytest.mark.parametrize("M,C,F,dt", [(70, 16, 16, BF16), (70, 136, 24, BF16), (70, 300, 100, BF16), (1, 16, 16, BF16),
+                                      (70, 16, 16, FP32), (7000, 136, 24, FP32)], ids=str)
 @pytest.mark.parametrize("act", ["silu", "gelu"])
-@pytest.mark.parametrize("C,F", [(16, 16), (136, 24), (300, 100)])
-def test_a_sum_past_the_range_is_a_closed_gate(C, F, act):
+def test_a_sum_past_the_range_is_a_closed_gate(M, C, F, dt, act):
     """G = -6e38, which fp32 does not hold: act's limit, not 0 times infinity."""
-    x, wg, wu, wd = inputs(torch.tensor([[-3e38, 1.0]] * 70), C, F, BF16)
+    x, wg, wu, wd = inputs(torch.tensor([[-3e38, 1.0]] * M), C, F, dt)
     x[:, 2] = x[:, 0]
     wg[:, 2] = 1.0
     y = evo.transition(x, wg, wu, wd, act=act)

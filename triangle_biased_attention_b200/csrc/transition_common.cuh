@@ -19,32 +19,43 @@
 
 namespace evo {
 
-// 1 / (1 + e^-g).  __expf and __fdividef are within 2 ulp or so of fp32 here;
-// e^-g overflows to inf below g = -88, which gives 0, the right limit.
-__device__ __forceinline__ float tr_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// sigmoid(g) from e^-|g| <= 1, which cannot overflow and goes to 0 with e^g on the
+// negative side.  expf's error is an ulp or so (__expf's grows with |g|, to 100 ulp at
+// g = -85, and all of it would reach act(g) there); __fdividef is within 2 ulp for
+// denominators as here, from 1 to 2.
+__device__ __forceinline__ float tr_sigmoid(float g) {
+    const float e = expf(-fabsf(g));
+    return __fdividef(g < 0.0f ? e : 1.0f, 1.0f + e);
+}
+
+// A gate as a factor of its sigmoid or Phi: finite, so that a sum G that has
+// overflowed gives act's limits, 0 and (times a factor or rounded) infinity, and not 0
+// times infinity.  NaN stays.
+__device__ __forceinline__ float tr_finite(float g) {
+    const float big = 3.402823466e38f;
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(big));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-big));
+    return g;
+}
 
 // act(g) and its derivative.  silu: g s, s (1 + g (1 - s)) with s = sigmoid(g);
 // gelu: g Phi(g), Phi(g) + g phi(g), Phi and phi the normal distribution and density.
 template <int ACT>
 __device__ __forceinline__ float tr_act(float g) {
-    if constexpr (ACT == EVO_ACT_SILU) {
-        return g < -88.0f ? 0.0f : g * tr_sigmoid(g);
-    } else {
-        return 0.5f * g * erfcf(-0.70710678118654752f * g);
-    }
+    if constexpr (ACT == EVO_ACT_SILU) return tr_finite(g) * tr_sigmoid(g);
+    else return tr_finite(g) * (0.5f * erfcf(-0.70710678118654752f * g));
 }
 
 template <int ACT>
 __device__ __forceinline__ void tr_act_grad(float g, float& a, float& da) {
     if constexpr (ACT == EVO_ACT_SILU) {
-        const float s = g < -88.0f ? 0.0f : tr_sigmoid(g);
-        a = g * s;
+        const float s = tr_sigmoid(g);
+        a = tr_finite(g) * s;
         da = fmaf(a, 1.0f - s, s);
-        if (g < -88.0f) a = da = 0.0f;
     } else {
         const float phi = 0.5f * erfcf(-0.70710678118654752f * g);
-        a = g * phi;
-        da = fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), phi);
+        a = tr_finite(g) * phi;
+        da = fmaf(tr_finite(g) * 0.3989422804014327f, expf(-0.5f * g * g), phi);
     }
 }
 

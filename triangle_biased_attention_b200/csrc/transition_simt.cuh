@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_grad_kernel(const TrSi
             float a, da;
             tr_act_grad<ACT>(g[e], a, da);
             h[e] = a * u[e];
-            dg[e] = d[e] * u[e] * da;
+            dg[e] = u[e] * da * d[e];  // (d u may overflow where act' is 0)
             du[e] = d[e] * a;
         }
         const long long at = (long long)m * p.F + f;

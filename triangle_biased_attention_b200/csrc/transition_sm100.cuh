@@ -158,16 +158,7 @@ __device__ __forceinline__ bool tr_near(const float (&g)[N]) {
     return m[0] <= kTrNear;
 }
 
-// A gate as a factor of its sigmoid or Phi: finite, so that a sum G that has
-// overflowed gives act's limits, 0 and (rounded) infinity, and not 0 times infinity.
-__device__ __forceinline__ float2 tr_finite2(float2 g) {
-    const float big = 3.402823466e38f;
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(g.x) : "f"(big));
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(g.y) : "f"(big));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.x) : "f"(-big));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g.y) : "f"(-big));
-    return g;
-}
+__device__ __forceinline__ float2 tr_finite2(float2 g) { return make_float2(tr_finite(g.x), tr_finite(g.y)); }
 
 // Phi(-|g|) e^(g^2/2) = t (c0 + c1 t + .. + c6 t^6), t = 1 / (1 + kPhiT |g|): fitted for the
 // smallest relative error on |g| <= 13.3, where e^(-g^2/2) leaves fp32's normal numbers
