@@ -373,10 +373,12 @@ EVO_API int64_t evo_transition_bwd_workspace_size(int64_t M, int64_t C, int64_t 
  *
  * Arithmetic: every product is accumulated in fp32 and the activation is
  * computed in fp32, with an error of a few roundings relative to act(G) on both
- * sides; a G past fp32's range gives act's limit (0 below).  With bf16 and fp16, H is rounded to the type before the
- * last product (its tensor-core operand), except in the form for a few rows,
- * which keeps it in fp32; with fp16 an |H| past 65504 is infinite.  Y is
- * rounded once.  The same call gives the same bits every time.
+ * sides; a G past fp32's range gives act's limit (0 below).  With bf16 and
+ * fp16, H is rounded to the type before the last product (its tensor-core
+ * operand), except in the form for a few rows, which keeps it in fp32 (so a row
+ * may come out rounded otherwise in a call of more rows); with fp16 an |H| past
+ * 65504 is infinite.  Y is rounded once.  The same call gives the same bits every
+ * time.
  *
  * Supported envelope: M < 2^31, C and F <= 2^20.  16-bit tensors 16-byte
  * aligned when C and F are multiples of 8, else 2-byte aligned; fp32 tensors

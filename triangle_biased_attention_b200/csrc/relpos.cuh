@@ -275,21 +275,22 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     const T* tile = p.dpair + ((long long)bh * p.Sq + i0) * p.Sk;  // row i of the tile: 32-bit offsets (ti * Sk < 2^31)
     const int *posq = p.pos_q + (long long)b * p.Sq + i0, *chainq = CHAINS ? p.chain_q + (long long)b * p.Sq + i0 : nullptr;
     constexpr int WORDS = VEC ? COLS * int(sizeof(T)) / 4 : COLS;  // a row's values as loaded
-    auto fetch = [&](int i, uint32_t (&w)[WORDS]) {  // row i, or the last one once more
-        const uint32_t at = uint32_t(min(i, rows - 1)) * uint32_t(p.Sk);
+    auto fetch = [&](int i, uint32_t (&w)[WORDS]) {  // row i; zeros behind the last one
+        const uint32_t at = uint32_t(i) * uint32_t(p.Sk);
+        const int end = i < rows ? p.Sk : 0;
         if constexpr (VEC) {
 #pragma unroll
             for (int k = 0; k < WORDS / 4; ++k) {
                 const int j = col(k * RUN);
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (j < p.Sk) x = *reinterpret_cast<const uint4*>(tile + (at + uint32_t(j)));
+                if (j < end) x = *reinterpret_cast<const uint4*>(tile + (at + uint32_t(j)));
                 w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
             }
         } else {
 #pragma unroll
             for (int e = 0; e < COLS; ++e) {
                 const int j = col(e);
-                w[e] = j < p.Sk ? __float_as_uint(rel_f32(tile[at + uint32_t(j)])) : 0u;
+                w[e] = j < end ? __float_as_uint(rel_f32(tile[at + uint32_t(j)])) : 0u;
             }
         }
     };
@@ -342,7 +343,8 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     }
     const uint32_t apart = offset(p.nb + 1);
     int pq = ty < rows ? posq[ty] : 0, cq = CHAINS && ty < rows ? chainq[ty] : 0;
-    for (int i = ty; i < rows; i += di) {
+    // every lane as often as the others: one whose rows are all done adds zeros
+    for (int i = ty; i - ty < rows; i += di) {
         fetch(i + 2 * di, after);
         const int pq_next = posq[min(i + di, rows - 1)], cq_next = CHAINS ? chainq[min(i + di, rows - 1)] : 0;
         uint32_t r[COLS], moved = 0;
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
             if (CHAINS && cq != ck[e]) r[e] = apart;
             moved |= r[e] ^ cur[e];
         }
-        if (__any_sync(__activemask(), moved != 0)) {
+        if (__any_sync(0xffffffffu, moved != 0)) {
 #pragma unroll
             for (int e = 0; e < COLS; ++e) {
                 flush(cur[e], sum[e]);
