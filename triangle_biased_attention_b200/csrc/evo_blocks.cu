@@ -857,8 +857,9 @@ RelTiles rel_bwd_tiles(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t row
     const int64_t held = std::min<int64_t>(5, (226 << 10) / (1024 + evo::rel_bwd_smem(int(std::min<int64_t>(rows, evo::kRelBins)), int(rows))));
     const int64_t want = std::max<int64_t>(1, 148 * std::max<int64_t>(1, held) / others);
     int64_t ti = std::max<int64_t>((Sq + want - 1) / want, 8 * per);
-    ti = std::max<int64_t>(ti, (Sq + 65534) / 65535);
     ti = (ti + per - 1) / per * per;
+    // at most so many rows a thread, which bounds the depth of its fp32 sums
+    ti = std::min<int64_t>(ti, evo::kRelBwdRows * per);
     // element offsets inside a tile are 32-bit (Sk < 2^29, and below 1024 unless `per` is 1)
     t.ti = int(std::min<int64_t>(ti, kIntMax / Sk / per * per));
     t.it = (Sq + t.ti - 1) / t.ti;
@@ -915,7 +916,9 @@ int run_relpos_bwd(int dev, evo::RelParams<T> p, const void* dpair, void* dtable
     if (!attrs[2 * vec + chains].ensure(dev, kernel, evo::rel_bwd_smem(evo::kRelBins, evo::kRelMaxBorders)))
         return EVO_ERR_CUDA;
     const int smem = evo::rel_bwd_smem(std::min(p.rows, evo::kRelBins), p.nb);
-    const dim3 grid{unsigned(t.jt), unsigned(t.it), unsigned(p.B * p.H * t.chunks)};
+    p.jt = int(t.jt);
+    p.it = int(t.it);
+    const dim3 grid{unsigned(t.jt * t.it), unsigned(p.B * p.H * t.chunks)};
     // (not dependent itself: its one wave of blocks would be laid out around the
     // blocks of the kernel before; 1733 x 1733 x 16 heads: 101 instead of 69 us)
     return launch(kernel, grid, evo::kRelBwdThreads, smem, st, p) &&
@@ -1006,8 +1009,8 @@ extern "C" EVO_API int evo_relpos_bwd(const void* dpair, const int32_t* borders,
     }
     if (!dpair || (!borders && num_borders > 0) || !pos_q || !pos_k || !workspace) return EVO_ERR_INVALID_ARG;
     const RelTiles t = rel_bwd_tiles(B, Sq, Sk, H, rows);
-    // the grid's z and y dimensions
-    if (B * H * t.chunks > 65535 || t.it > 65535) return EVO_ERR_UNSUPPORTED_SHAPE;
+    // the grid's y and x dimensions
+    if (B * H * t.chunks > 65535 || t.it * t.jt > kIntMax) return EVO_ERR_UNSUPPORTED_SHAPE;
     if (workspace_bytes < t.part_bytes) return EVO_ERR_INVALID_ARG;
     if (!aligned(dpair, uintptr_t(es)) || !aligned(workspace, 256)) return EVO_ERR_MISALIGNED;
     for (const int32_t* p : {borders, pos_q, pos_k, chain_q, chain_k})

@@ -28,6 +28,7 @@ constexpr int kRelThreads = 256;      // forward
 constexpr int kRelCols = 8;           // key columns of a forward thread
 constexpr int kRelBwdThreads = 128;   // backward
 constexpr int kRelBwdCols = 8;        // key columns of a backward thread
+constexpr int kRelBwdRows = 480;      // most query rows of a backward thread
 constexpr int kRelLut = 2048;         // entries of the distance table
 constexpr int kRelMaxBorders = 2048;
 constexpr int kRelBins = 256;         // table rows that one backward block sums
@@ -43,6 +44,7 @@ struct RelParams {
     int B, Sq, Sk, H, nb, rows;
     int ti;               // query rows of a block
     int lane_cols;        // log2 of the threads along j
+    int jt, it;           // backward: tiles along j and along i
     int groups;           // forward: groups of heads
 };
 
@@ -232,7 +234,9 @@ __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const Re
 // One block: `ti` query rows x 128 threads' key columns of one head, table rows
 // [bin0, bin0 + kRelBins).  Each thread sums into its own column of shared
 // memory, [bin][thread], so no two threads meet and the order of the additions
-// is fixed.  While no column of a warp leaves its bucket the sums stay in
+// is fixed.  A bin takes up to one addition for each of a thread's columns and rows, 8
+// x kRelBwdRows = 3840, and 7 more across the threads: the depth of the fp32 sums is below
+// 4096 at every size, and the tiles are added in fp64.  While no column of a warp leaves its bucket the sums stay in
 // registers; when one does, the warp adds all of them to their bins, without a
 // branch for each (branches for each column, or taking only the columns that
 // moved, took 5 times as long: near the diagonal most rows move some column).
@@ -256,10 +260,10 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     constexpr int COLS = kRelBwdCols;
     constexpr int ROW = kRelBwdThreads * 4;  // bytes of a bin
     extern __shared__ __align__(16) uint8_t rel_sm[];
-    const int jt = blockIdx.x, itile = blockIdx.y;
+    const int jt = blockIdx.x % p.jt, itile = blockIdx.x / p.jt;
     const int chunks = (p.rows + kRelBins - 1) / kRelBins;
-    const int bin0 = (blockIdx.z % chunks) * kRelBins, nbins = min(kRelBins, p.rows - bin0);
-    const int bh = blockIdx.z / chunks, b = bh / p.H, h = bh % p.H;
+    const int bin0 = (blockIdx.y % chunks) * kRelBins, nbins = min(kRelBins, p.rows - bin0);
+    const int bh = blockIdx.y / chunks, b = bh / p.H, h = bh % p.H;
     float* bins = reinterpret_cast<float*>(rel_sm);  // [nbins + 1][128]
     int* sborders = reinterpret_cast<int*>(bins + (min(p.rows, kRelBins) + 1) * kRelBwdThreads);
     uint32_t* lut = reinterpret_cast<uint32_t*>(sborders + (p.nb + 3) / 4 * 4);
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     __syncthreads();
     // the 128 columns of each bin, a warp a bin, in a fixed order
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long slot = ((long long)b * gridDim.y + itile) * gridDim.x + jt;
+    const long long slot = ((long long)b * p.it + itile) * p.jt + jt;
 #pragma unroll 4
     for (int r = warp; r < nbins; r += kRelBwdThreads / 32) {
         const float4 x = reinterpret_cast<const float4*>(bins + r * kRelBwdThreads)[lane];
@@ -393,7 +397,8 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     }
 }
 
-// dtable[r, h] = the sum over the tiles, a warp an element, in a fixed order.  (No
+// dtable[r, h] = the sum over the tiles, a warp an element, in a fixed order, in fp64 (there
+// may be any number of tiles; one addition for each is too few to matter).  (No
 // restrict pointers where a kernel waits for the one before: a read could move
 // ahead of the wait.)
 template <typename T>
@@ -405,11 +410,11 @@ __global__ void __launch_bounds__(256) evo_relpos_bwd_sum_kernel(const float* pa
     const int lane = threadIdx.x & 31;
     if (w >= (long long)H * rows) return;
     const int h = int(w / rows), r = int(w % rows);
-    float s = 0.0f;
+    double s = 0.0;
     for (long long t = lane; t < tiles; t += 32) s += part[(t * H + h) * rows + r];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) dtable[(long long)r * H + h] = rel_from<T>(s);
+    if (lane == 0) dtable[(long long)r * H + h] = rel_from<T>(float(s));
 }
 
 }  // namespace evo
