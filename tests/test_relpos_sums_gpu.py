@@ -68,3 +68,16 @@ def test_sums_over_many_batches(B):
     want = np.array([[0.0], [value * B * 128 * 128]])
     gamma = DEPTH * 2.0 ** -24 / (1 - DEPTH * 2.0 ** -24)
     assert (np.abs(got - want) <= (gamma + 2.0 ** -24) * want).all(), got[1, 0] / want[1, 0] - 1
+
+
+@pytest.mark.parametrize("B,H,dt,extra", [(20001, 16, FP32, True), (33000, 9, BF16, False), (65535, 3, FP16, True)], ids=str)
+def test_more_batches_and_heads_than_a_grid_dimension(B, H, dt, extra):
+    """Batches times groups of heads past 65535: each batch with its own positions, chains and base."""
+    table, borders, pq, pk, cq, ck, pair = make(B, 2, 3, H, 7, dt, seed=B, chains=extra)
+    base = pair if extra else None
+    p = evo.relpos_bias(table, borders, pq, pk, cq, ck, base=base)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    ref, (r, tiny) = R.forward(table, borders, pq, pk, cq, ck, base), units(dt)
+    # exact without a base; with one an fp32 sum and a rounding
+    err = (r + 2.0 ** -24) * (1 + 2.0 ** -7) * np.abs(ref) + tiny if extra else 0.0
+    assert (np.abs(_f64(p) - ref) <= err).all()

@@ -879,13 +879,25 @@ int launch_relpos_fwd(int dev, evo::RelParams<T> p, cudaStream_t st) {
     int64_t ti = (p.Sq * others + 148 * 6 - 1) / (148 * 6);
     ti = std::max<int64_t>(ti, (int64_t(p.Sq) + 65534) / 65535);
     p.ti = int((ti + per - 1) / per * per);
-    if (int64_t(p.B) * p.groups > 65535) return EVO_ERR_UNSUPPORTED_SHAPE;
     const int smem = evo::rel_smem((p.rows * NW * 4 + 15) / 16 * 16, p.nb);
     auto kernel = evo::evo_relpos_fwd_kernel<T, NW, VEC>;
     static AttrOnce attr;
     if (!attr.ensure(dev, kernel, evo::rel_smem((evo::kRelMaxBorders + 4) * NW * 4, evo::kRelMaxBorders))) return EVO_ERR_CUDA;
-    const dim3 grid{unsigned(jt), blocks_of(p.Sq, p.ti), unsigned(p.B * p.groups)};
-    return launch_dependent(kernel, grid, evo::kRelThreads, smem, st, p) ? EVO_OK : EVO_ERR_CUDA;
+    // as many batches at once as the grid's z dimension takes with their groups of heads
+    const int step = std::max(1, 65535 / p.groups), all = p.B;
+    for (int b = 0; b < all; b += step) {
+        p.B = std::min(step, all - b);
+        if (!launch_dependent(kernel, dim3(unsigned(jt), blocks_of(p.Sq, p.ti), unsigned(p.B * p.groups)), evo::kRelThreads, smem, st, p))
+            return EVO_ERR_CUDA;
+        const int64_t pairs = int64_t(p.B) * p.H * p.Sq * p.Sk;
+        p.pos_q += int64_t(p.B) * p.Sq;
+        p.pos_k += int64_t(p.B) * p.Sk;
+        if (p.chain_q) p.chain_q += int64_t(p.B) * p.Sq;
+        if (p.chain_k) p.chain_k += int64_t(p.B) * p.Sk;
+        if (p.base) p.base += pairs;
+        p.pair += pairs;
+    }
+    return EVO_OK;
 }
 
 template <typename T>
