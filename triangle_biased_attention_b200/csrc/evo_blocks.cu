@@ -855,11 +855,14 @@ RelTiles rel_bwd_tiles(int64_t B, int64_t Sq, int64_t Sk, int64_t H, int64_t row
     const int64_t others = std::max<int64_t>(1, B * H * t.jt * t.chunks);
     // one wave: a block's shared memory sets how many an SM holds (five by their registers)
     const int64_t held = std::min<int64_t>(5, (226 << 10) / (1024 + evo::rel_bwd_smem(int(std::min<int64_t>(rows, evo::kRelBins)), int(rows))));
-    const int64_t want = std::max<int64_t>(1, 148 * std::max<int64_t>(1, held) / others);
+    // at most kRelBwdRows rows a thread, which bounds the depth of its fp32 sums; where one
+    // wave of blocks would have more, as few whole waves as keep to it (8192 x 8192 x 8
+    // heads, us: 2 waves of 357 rows 386, 1.6 waves of 480 rows 502, one wave of 745 393)
+    const int64_t most = evo::kRelBwdRows * per, wave = 148 * std::max<int64_t>(1, held);
+    const int64_t waves = std::max<int64_t>(1, ((Sq + most - 1) / most * others + wave - 1) / wave);
+    const int64_t want = std::max<int64_t>(1, wave * waves / others);
     int64_t ti = std::max<int64_t>((Sq + want - 1) / want, 8 * per);
-    ti = (ti + per - 1) / per * per;
-    // at most so many rows a thread, which bounds the depth of its fp32 sums
-    ti = std::min<int64_t>(ti, evo::kRelBwdRows * per);
+    ti = std::min<int64_t>((ti + per - 1) / per * per, most);
     // element offsets inside a tile are 32-bit (Sk < 2^29, and below 1024 unless `per` is 1)
     t.ti = int(std::min<int64_t>(ti, kIntMax / Sk / per * per));
     t.it = (Sq + t.ti - 1) / t.ti;
