@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const Re
 // One block: `ti` query rows x 128 threads' key columns of one head, table rows
 // [bin0, bin0 + kRelBins).  Each thread sums into its own column of shared
 // memory, [bin][thread], so no two threads meet and the order of the additions
-// is fixed.  A bin takes up to one addition for each of a thread's columns and rows, 8
-// x kRelBwdRows = 3840, and 7 more across the threads: the depth of the fp32 sums is below
-// 4096 at every size, and the tiles are added in fp64.  While no column of a warp leaves its bucket the sums stay in
+// is fixed.  A bin takes up to one addition for each of a thread's columns and rows,
+// 8 x kRelBwdRows = 3840, and 9 more across threads and tiles: the fp32 sums are less than
+// 4096 additions deep at every size.  While no column of a warp leaves its bucket the sums stay in
 // registers; when one does, the warp adds all of them to their bins, without a
 // branch for each (branches for each column, or taking only the columns that
 // moved, took 5 times as long: near the diagonal most rows move some column).
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const Re
 // beside the memory, so the distance table holds the bins' byte offsets (a row of
 // another range of bins: the one behind the last, which nobody reads) and the
 // positions are kept as byte offsets into it: an element costs a subtraction, a
-// clamp, a read and an addition.  1733 x 1733 x 16 heads, fp32: 67 us, 192 MB, 2.85 TB/s, the
+// clamp, a read and an addition.  1733 x 1733 x 16 heads, fp32: 67.6 us, 192 MB, 2.84 TB/s, the
 // issue slots 67 % busy (an odd row length allows 4-byte loads only, and log-spaced
 // buckets move some column of a warp in most rows).  That needs positions below 2^27 in size and
 // borders within the table's span; other blocks search the borders.
@@ -279,27 +279,29 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     const T* tile = p.dpair + ((long long)bh * p.Sq + i0) * p.Sk;  // row i of the tile: 32-bit offsets (ti * Sk < 2^31)
     const int *posq = p.pos_q + (long long)b * p.Sq + i0, *chainq = CHAINS ? p.chain_q + (long long)b * p.Sq + i0 : nullptr;
     constexpr int WORDS = VEC ? COLS * int(sizeof(T)) / 4 : COLS;  // a row's values as loaded
-    auto fetch = [&](int i, uint32_t (&w)[WORDS]) {  // row i; zeros behind the last one
-        const uint32_t at = uint32_t(i) * uint32_t(p.Sk);
-        const int end = i < rows ? p.Sk : 0;
+    auto fetch = [&](int i, uint32_t (&w)[WORDS]) {  // row i, or the last one once more
+        const uint32_t at = uint32_t(min(i, rows - 1)) * uint32_t(p.Sk);
         if constexpr (VEC) {
 #pragma unroll
             for (int k = 0; k < WORDS / 4; ++k) {
                 const int j = col(k * RUN);
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (j < end) x = *reinterpret_cast<const uint4*>(tile + (at + uint32_t(j)));
+                if (j < p.Sk) x = *reinterpret_cast<const uint4*>(tile + (at + uint32_t(j)));
                 w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
             }
         } else {
 #pragma unroll
             for (int e = 0; e < COLS; ++e) {
                 const int j = col(e);
-                w[e] = j < end ? __float_as_uint(rel_f32(tile[at + uint32_t(j)])) : 0u;
+                if constexpr (sizeof(T) == 4) w[e] = j < p.Sk ? __float_as_uint(tile[at + uint32_t(j)]) : 0u;
+                else w[e] = j < p.Sk ? reinterpret_cast<const uint16_t*>(tile)[at + uint32_t(j)] : 0u;
             }
         }
     };
     auto value = [&](const uint32_t (&w)[WORDS], int e) -> float {
-        if constexpr (!VEC || sizeof(T) == 4) return __uint_as_float(w[e]);
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        else if constexpr (!VEC && std::is_same<T, __half>::value) return __half2float(__ushort_as_half(uint16_t(w[e])));
+        else if constexpr (!VEC) return ptx::bf16lo_to_f32(w[e]);
         else if constexpr (std::is_same<T, __half>::value) return __half2float(reinterpret_cast<const __half*>(w)[e]);
         else return e & 1 ? ptx::bf16hi_to_f32(w[e / 2]) : ptx::bf16lo_to_f32(w[e / 2]);
     };
@@ -347,8 +349,7 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     }
     const uint32_t apart = offset(p.nb + 1);
     int pq = ty < rows ? posq[ty] : 0, cq = CHAINS && ty < rows ? chainq[ty] : 0;
-    // every lane as often as the others: one whose rows are all done adds zeros
-    for (int i = ty; i - ty < rows; i += di) {
+    auto step = [&](int i) {  // row i; all lanes of a warp take part
         fetch(i + 2 * di, after);
         const int pq_next = posq[min(i + di, rows - 1)], cq_next = CHAINS ? chainq[min(i + di, rows - 1)] : 0;
         uint32_t r[COLS], moved = 0;
@@ -380,6 +381,15 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
         for (int k = 0; k < WORDS; ++k) w[k] = next[k], next[k] = after[k];
         pq = pq_next;
         cq = cq_next;
+    };
+    int first_row = 0;  // of those that the block's threads take at once
+    for (; first_row + di <= rows; first_row += di) step(first_row + ty);
+    if (first_row < rows) {  // some lanes have no row left: they add zeros
+        if (first_row + ty >= rows) {
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) w[k] = 0u;
+        }
+        step(first_row + ty);
     }
 #pragma unroll
     for (int e = 0; e < COLS; ++e) flush(cur[e], sum[e]);
@@ -397,10 +407,9 @@ __global__ void __launch_bounds__(kRelBwdThreads, 5) evo_relpos_bwd_kernel(const
     }
 }
 
-// dtable[r, h] = the sum over the tiles, a warp an element, in a fixed order, in fp64 (there
-// may be any number of tiles; one addition for each is too few to matter).  (No
-// restrict pointers where a kernel waits for the one before: a read could move
-// ahead of the wait.)
+// dtable[r, h] = the sum over the tiles, a warp an element, in a fixed order: four at a
+// time in fp32, then in fp64, because there may be any number of tiles.  (No restrict
+// pointers where a kernel waits for the one before: a read could move ahead of the wait.)
 template <typename T>
 __global__ void __launch_bounds__(256) evo_relpos_bwd_sum_kernel(const float* part, long long tiles, int H,
                                                                  int rows, T* dtable) {
@@ -411,7 +420,12 @@ __global__ void __launch_bounds__(256) evo_relpos_bwd_sum_kernel(const float* pa
     if (w >= (long long)H * rows) return;
     const int h = int(w / rows), r = int(w % rows);
     double s = 0.0;
-    for (long long t = lane; t < tiles; t += 32) s += part[(t * H + h) * rows + r];
+    for (long long t = lane; t < tiles; t += 128) {  // four on their way at a time, added in pairs first
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = t + 32 * k < tiles ? part[((t + 32 * k) * H + h) * rows + r] : 0.0f;
+        s += (v[0] + v[1]) + (v[2] + v[3]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) dtable[(long long)r * H + h] = rel_from<T>(float(s));
