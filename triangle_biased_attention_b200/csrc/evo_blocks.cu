@@ -85,6 +85,74 @@ int64_t tr_chunk_rows(int64_t M, int64_t row_bytes, bool backward) {
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
+// fp32 products in parts: tiles of `rows` x `cols`, `splits` ranges of K with slots of
+// their own (0: the kernel without parts).
+struct TrPart {
+    int rows = 128, cols = 128, splits = 0;
+};
+
+// Estimated microseconds of one 16-deep slab of a block's walk over K: with one block on an SM,
+// for each of several, and how much longer where the rows are no whole 16-byte units.
+// Measured at 1184 to 16384 rows, 512 x 1024 and 509 x 1021; blocks of one SM take turns on its
+// shared memory and FMA units, so two take about twice as long as one.
+struct TrTile {
+    int rows, cols;
+    double lone, shared, odd;
+};
+constexpr TrTile kTrTiles[] = {{128, 128, 1.95, 1.72, 1.07}, {128, 64, 1.08, 1.0, 1.17}, {32, 128, 0.95, 0.74, 1.15}};
+constexpr TrTile kTrGate = {128, 64, 2.35, 1.84, 1.2}, kTrGrad = {128, 64, 2.85, 2.77, 1.15}, kTrDw = {128, 128, 3.1, 1.65, 1.13};
+
+double tr_walk(const TrTile& t, int64_t blocks, int64_t K, bool odd) {
+    const int64_t per = (blocks + 147) / 148;
+    return double((K + evo::kTrK - 1) / evo::kTrK) * (per == 1 ? t.lone : double(per) * t.shared) * (odd ? t.odd : 1.0);
+}
+
+int64_t tr_tiles(const TrTile& t, int64_t rows, int64_t cols) { return (rows + t.rows - 1) / t.rows * ((cols + t.cols - 1) / t.cols); }
+
+// Time of the kernels without parts.
+double tr_gate_time(int64_t rows, int64_t C, int64_t F, bool backward) {
+    const TrTile& t = backward ? kTrGrad : kTrGate;
+    return tr_walk(t, tr_tiles(t, rows, F), C, C % 4 != 0);
+}
+double tr_out_time(int64_t rows, int64_t C, int64_t F, bool backward) {
+    const TrTile& t = kTrTiles[tr_tiles(kTrTiles[0], rows, C) < 2 * 148 ? 1 : 0];
+    return tr_walk(t, tr_tiles(t, rows, C), backward ? 2 * F : F, (backward ? C : F) % 4 != 0);
+}
+
+// The tile and ranges of `jobs` products [rows, K] x [K, N] in parts, or none where the
+// kernel without parts (`whole`) is estimated faster.
+TrPart tr_parts(int64_t rows, int64_t N, int64_t K, int64_t jobs, bool odd, double whole) {
+    TrPart best;
+    double least = 0.95 * whole;  // (what an estimate may be off by is not worth two launches)
+    for (const TrTile& t : kTrTiles)
+        for (int splits = 1; splits <= 64; ++splits) {
+            const int64_t slabs = (K + splits * evo::kTrK - 1) / (splits * evo::kTrK);
+            const double bytes = 4.0 * double(rows) * double(N) * double(jobs) * splits;  // of the slots
+            if ((splits > 1 && slabs < 2) || bytes > 128e6 || (rows + t.rows - 1) / t.rows > 65535) break;
+            // another launch, the host's side of it included, and the slots read at 4 TB/s
+            const double time = tr_walk(t, tr_tiles(t, rows, N) * jobs * splits, slabs * evo::kTrK, odd) + 7.0 + bytes / 4e6;
+            if (time < least) {
+                least = time;
+                best.rows = t.rows, best.cols = t.cols, best.splits = splits;
+            }
+        }
+    return best;
+}
+
+// Ranges of rows of the weight gradients, each with slots of its own: as estimated
+// fastest, with the slots written and read at 4 TB/s.
+int64_t tr_dw_splits(int64_t rows, int64_t C, int64_t F) {
+    int64_t best = 1;
+    double least = 0;
+    for (int64_t splits = 1; splits <= 128; ++splits) {
+        const int64_t per = (rows + splits - 1) / splits;
+        if (splits > 1 && per < 4 * evo::kTrK) break;
+        const double time = tr_walk(kTrDw, 3 * tr_tiles(kTrDw, F, C) * splits, per, C % 4 != 0) + double(splits) * 24.0 * double(C) * double(F) / 4e6;
+        if (splits == 1 || time < least) least = time, best = splits;
+    }
+    return best;
+}
+
 struct TrLayout {
     int64_t chunk = 0;                            // rows of a chunk
     int64_t h = 0, dg = 0, du = 0;                // [chunk, F] (16-bit: rows up to 128, F up to 128)
@@ -92,6 +160,8 @@ struct TrLayout {
     bool direct = false;                          // 16-bit: the last products are the weight gradients
     int64_t splits = 0, split_rows = 0;           // ranges of rows with a slot of their own
     bool gradw = false;                           // the backward that keeps weight gradients on chip: no H, [C, F up to 64] slots
+    TrPart grad, out;                             // fp32: G, U (and dH); Y or dX
+    int64_t slots = 0;                            // their slots, one after the other
     bool few = false;                             // the forward's form for a few rows: H [M, F] in fp32
     bool fused = false;                           // the forward's one-kernel form: no [M, F] array at all
     int64_t x = 0, dy = 0, wg = 0, wu = 0, wd = 0;  // 16-bit, odd C or F: copies with rows of whole 16-byte units
@@ -103,14 +173,20 @@ struct TrLayout {
 // 16-bit, us, against the tensor cores: one row 2.9 / 5.3 (C = 64, F = 256) to 11.3 / 20.5
 // (1024, 4096); 4 rows 5.1 / 7.1 (128, 512), 11.1 / 9.2 (256, 1024); 8 rows 7.5 / 7.1 (128, 512);
 // where rows would have to be copied for TMA first, 8 rows 8.3 / 9.5 (100, 397), 14.9 / 16.7
-// (388, 1555). With fp32 its time grows with
-// M C F, while the tiles' is that of one tile's walk over C and F until the rows
-// fill the SMs. Measured, us, groups against tiles: C = 128, F = 512: 16 rows 9.5 / 49.5,
-// 256 29 / 55; C = 384, F = 1536: 64 rows 52 / 143, 192 135 / 155, 256 178 / 155; C = 464, F =
-// 1856: 128 rows 163 / 185, 192 237 / 188; C = 1024, F = 4096: 32 rows 188 / 377, 96 548 / 399.
+// (388, 1555). With fp32 its time grows with M C F, and with the features of each group where
+// rows of weights are short. Measured, us of the kernels, groups (two launches) against tiles in
+// parts (four, so that a call not in a graph takes 26 at least): C = 64, F = 256: 128 rows 13.4 / 15.3,
+// 256 18.0 / 15.4; C = 128, F = 512: 64 rows 15.8 / 16.7, 128 21.6 / 16.8; C = 256, F = 1024: 16 rows 17.5 /
+// 18.4, 32 24.5 / 18.7; C = 384, F = 1536: 4 rows 15.0 / 20.6, 16 24.8 / 21.0, 32 44.7 / 21.2; C = 752, F = 3008:
+// one row 14.2 / 32.9, 4 38.0 / 32.9 (odd rows read 4 bytes at a time, without bank
+// conflicts: 896 x 3494, 5 rows 30 / 51; 987 x 564, 20 rows 22 / 30); C = 16, F = 2775: 16 rows 21.9 / 17.5, 64
+// 38.6 / 18.6.
 bool tr_few(int64_t M, int64_t C, int64_t F, int dtype) {
     if (8 * C * 4 > evo::kTrFewBytes || 8 * F * 4 > evo::kTrFewBytes) return false;
-    if (dtype == EVO_DTYPE_FP32) return M <= evo::kTrFewRows || M * C * F <= 50000 * (C + F);
+    if (dtype == EVO_DTYPE_FP32) {
+        const int64_t most = C % 4 == 0 && F % 4 == 0 ? 10000000 : 26000000;
+        return M <= 4 || (M * C * F <= most && (M + evo::kTrFewRows - 1) / evo::kTrFewRows * F <= 15000);
+    }
     if (C % 8 == 0 && F % 8 == 0) return M == 1 || (M <= 4 && C * F <= 100000);
     return M == 1 || (M <= evo::kTrFewRows && C * F <= 700000);
 }
@@ -145,7 +221,7 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
         L->total = round_up(M * F * 4, 256);
         return true;
     }
-    const int64_t ldf = dtype == EVO_DTYPE_FP32 ? F : round_up(F, 128);
+    const int64_t ldf = round_up(F, dtype == EVO_DTYPE_FP32 ? 4 : 128);
     L->pad = dtype != EVO_DTYPE_FP32 && (C % 8 != 0 || F % 8 != 0);
     L->fused = !backward && tr_fused(M, C, F, dtype);
     L->gradw = backward && tr_gradw(C, dtype);
@@ -160,13 +236,18 @@ bool tr_layout(int64_t M, int64_t C, int64_t F, int dtype, bool backward, TrLayo
         return at;
     };
     if (!L->fused && !L->gradw) L->h = take(hbytes);
+    if (dtype == EVO_DTYPE_FP32) {
+        const int64_t jobs = backward ? 3 : 2, sums = backward ? 2 : 1;
+        L->grad = tr_parts(L->chunk, F, C, jobs, C % 4 != 0, tr_gate_time(L->chunk, C, F, backward));
+        L->out = tr_parts(L->chunk, C, F, sums, (backward ? C : F) % 4 != 0, tr_out_time(L->chunk, C, F, backward));
+        const int64_t most = std::max(L->grad.splits * jobs * round_up(F, 4), L->out.splits * sums * round_up(C, 4));
+        L->slots = take(L->chunk * most * 4);
+    }
     if (backward) {
         L->dg = take(hbytes);
         L->du = take(hbytes);
         if (dtype == EVO_DTYPE_FP32) {
-            // enough ranges of rows for two blocks a SM, none under 512 rows
-            const int64_t tiles = 3 * ((F + 127) / 128) * ((C + 127) / 128);
-            L->splits = std::max<int64_t>(1, std::min((296 + tiles - 1) / tiles, (L->chunk + 511) / 512));
+            L->splits = tr_dw_splits(L->chunk, C, F);
             L->split_rows = (L->chunk + L->splits - 1) / L->splits;
             L->part = take(L->splits * 3 * fc * 4);
         } else if (L->gradw) {
@@ -255,6 +336,50 @@ bool launch_simt_out(const evo::TrSimtParams& p, cudaStream_t st) {
     return launch(evo::evo_tr_simt_out_kernel<BWD, 2>, dim3(blocks_of(p.C, 128), mt), evo::kTrThreads, kTrSmem, st, p);
 }
 
+// One stage of products in parts; the slots' sums are the caller's.
+template <int B_LAYOUT>
+bool launch_parts(const TrPart& t, evo::TrPartParams& p, cudaStream_t st) {
+    p.splits = t.splits;
+    p.ld = int(round_up(p.N, 4));
+    const dim3 grid(blocks_of(p.N, t.cols), blocks_of(p.rows, t.rows), unsigned(p.jobs * t.splits));
+    if (t.rows == 32) return launch(evo::evo_tr_simt_part_kernel<32, 2, B_LAYOUT>, grid, evo::kTrThreads, kTrSmem, st, p);
+    return t.cols == 128 ? launch(evo::evo_tr_simt_part_kernel<128, 2, B_LAYOUT>, grid, evo::kTrThreads, kTrSmem, st, p)
+                         : launch(evo::evo_tr_simt_part_kernel<128, 1, B_LAYOUT>, grid, evo::kTrThreads, kTrSmem, st, p);
+}
+
+// G and U (and dH with `backward`) in parts, then H (dG, dU).
+template <int ACT, bool BWD>
+bool run_gate_parts(const TrPart& t, const evo::TrSimtParams& p, float* slots, cudaStream_t st) {
+    evo::TrPartParams q = {};
+    q.jobs = BWD ? 3 : 2;
+    q.job[0] = {p.x, p.wg, p.C, true, p.vc, p.vc};
+    q.job[1] = {p.x, p.wu, p.C, true, p.vc, p.vc};
+    q.job[2] = {p.dy, p.wd, p.C, false, p.vc, p.vd};
+    q.rows = p.rows;
+    q.N = p.F;
+    q.K = p.C;
+    q.slots = slots;
+    return launch_parts<BWD ? evo::TR_B_MIXED : evo::TR_B_K>(t, q, st) &&
+           launch_any(false, evo::evo_tr_join_act_kernel<ACT, BWD>, dim3(blocks_of(int64_t(q.rows) * q.ld / 4, 256)), 256, 0, st,
+                      (const float*)slots, q.splits, q.rows, q.ld, p.h, p.dg, p.du);
+}
+
+// Y or dX in parts.
+template <bool BWD>
+bool run_out_parts(const TrPart& t, const evo::TrSimtParams& p, float* slots, cudaStream_t st) {
+    evo::TrPartParams q = {};
+    q.jobs = BWD ? 2 : 1;
+    q.job[0] = {BWD ? p.dg : p.h, BWD ? p.wg : p.wd, p.ldf, !BWD, true, BWD ? p.vc : p.vd};
+    q.job[1] = {p.du, p.wu, p.ldf, false, true, p.vc};
+    q.rows = p.rows;
+    q.N = p.C;
+    q.K = p.F;
+    q.slots = slots;
+    return launch_parts<BWD ? evo::TR_B_N : evo::TR_B_K>(t, q, st) &&
+           launch_any(false, evo::evo_tr_join_out_kernel, dim3(blocks_of(int64_t(q.rows) * q.ld / 4, 256)), 256, 0, st,
+                      (const float*)slots, q.jobs * q.splits, q.rows, q.N, q.ld, p.out, int(p.vo));
+}
+
 template <int ACT>
 int run_fwd_simt(const float* X, const float* Wg, const float* Wu, const float* Wd, float* Y, char* ws, int64_t M, int64_t C, int64_t F,
                  int dtype, cudaStream_t st) {
@@ -265,17 +390,21 @@ int run_fwd_simt(const float* X, const float* Wg, const float* Wu, const float* 
     p.wu = Wu;
     p.wd = Wd;
     p.h = reinterpret_cast<float*>(ws + L.h);
+    float* const slots = reinterpret_cast<float*>(ws + L.slots);
     p.C = int(C);
     p.F = int(F);
-    p.vec = C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
-            aligned(Wd, 16) && aligned(Y, 16);
+    p.ldf = int(round_up(F, 4));
+    p.vc = C % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16);
+    p.vd = F % 4 == 0 && aligned(Wd, 16);
+    p.vo = C % 4 == 0 && aligned(Y, 16);
     for (int64_t m = 0; m < M; m += L.chunk) {
         p.rows = int(std::min(L.chunk, M - m));
         p.x = X + m * C;
         p.out = Y + m * C;
         const unsigned mt = blocks_of(p.rows, 128);
-        if (!launch(evo::evo_tr_simt_gate_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
-            !launch_simt_out<false>(p, st))
+        if (!(L.grad.splits ? run_gate_parts<ACT, false>(L.grad, p, slots, st)
+                            : launch(evo::evo_tr_simt_gate_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p)) ||
+            !(L.out.splits ? run_out_parts<false>(L.out, p, slots, st) : launch_simt_out<false>(p, st)))
             return EVO_ERR_CUDA;
     }
     return EVO_OK;
@@ -294,13 +423,16 @@ int run_bwd_simt(const float* X, const float* Wg, const float* Wu, const float* 
     p.dg = reinterpret_cast<float*>(ws + L.dg);
     p.du = reinterpret_cast<float*>(ws + L.du);
     p.part = reinterpret_cast<float*>(ws + L.part);
+    float* const slots = reinterpret_cast<float*>(ws + L.slots);
     p.C = int(C);
     p.F = int(F);
     p.splits = int(L.splits);
     p.split_rows = int(L.split_rows);
     p.dw_mask = (dWg ? 1 : 0) | (dWu ? 2 : 0) | (dWd ? 4 : 0);
-    p.vec = C % 4 == 0 && F % 4 == 0 && aligned(X, 16) && aligned(Wg, 16) && aligned(Wu, 16) &&
-            aligned(Wd, 16) && aligned(dY, 16) && (!dX || aligned(dX, 16));
+    p.ldf = int(round_up(F, 4));
+    p.vc = C % 4 == 0 && aligned(X, 16) && aligned(dY, 16) && aligned(Wg, 16) && aligned(Wu, 16);
+    p.vd = F % 4 == 0 && aligned(Wd, 16);
+    p.vo = C % 4 == 0 && aligned(dX, 16);
     for (int64_t m = 0; m < M; m += L.chunk) {
         p.rows = int(std::min(L.chunk, M - m));
         p.x = X + m * C;
@@ -308,8 +440,9 @@ int run_bwd_simt(const float* X, const float* Wg, const float* Wu, const float* 
         p.out = dX ? dX + m * C : nullptr;
         p.first = m == 0;
         const unsigned mt = blocks_of(p.rows, 128), big = blocks_of(std::max(C, F), 128);
-        if (!launch(evo::evo_tr_simt_grad_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p) ||
-            (dX && !launch_simt_out<true>(p, st)) ||
+        if (!(L.grad.splits ? run_gate_parts<ACT, true>(L.grad, p, slots, st)
+                            : launch(evo::evo_tr_simt_grad_kernel<ACT>, dim3(blocks_of(F, 64), mt), evo::kTrThreads, kTrSmem, st, p)) ||
+            (dX && !(L.out.splits ? run_out_parts<true>(L.out, p, slots, st) : launch_simt_out<true>(p, st))) ||
             (p.dw_mask && !launch(evo::evo_tr_simt_dw_kernel, dim3(big, big, unsigned(3 * L.splits)),
                                   evo::kTrThreads, kTrSmem, st, p)))
             return EVO_ERR_CUDA;

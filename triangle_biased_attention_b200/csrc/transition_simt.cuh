@@ -97,10 +97,10 @@ __device__ __forceinline__ void tr_fma2(float2& c, float2 a, float2 b) {
 }
 
 // acc += A B^T over k in [kbeg, kend).  COLS: column groups computed (2, or 1
-// for a 64-column tile).  `smem` holds 4 slabs.
+// for a 64-column tile).  veca, vecb: 16-byte loads allowed.  `smem` holds 4 slabs.
 template <bool AKC, bool BKC, int COLS>
 __device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOperand& A, const TrOperand& B,
-                                        int kbeg, int kend, bool vec, float* smem) {
+                                        int kbeg, int kend, bool veca, bool vecb, float* smem) {
     constexpr int SLAB = kTrK * kTrLd;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float va[8], vb[8];
@@ -108,8 +108,8 @@ __device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOper
     TrFetch<BKC> fb(B, kbeg);
     __syncthreads();  // an earlier product's slabs are no longer read
     if (kbeg < kend) {
-        fa.load(va, kend, vec);
-        fb.load(vb, kend, vec);
+        fa.load(va, kend, veca);
+        fb.load(vb, kend, vecb);
         tr_put<AKC>(smem, va);
         tr_put<BKC>(smem + SLAB, vb);
     }
@@ -118,8 +118,8 @@ __device__ __forceinline__ void tr_tile(float2 (&acc)[8][2 * COLS], const TrOper
     for (int k0 = kbeg; k0 < kend; k0 += kTrK) {
         const bool more = k0 + kTrK < kend;
         if (more) {
-            fa.load(va, kend, vec);
-            fb.load(vb, kend, vec);
+            fa.load(va, kend, veca);
+            fb.load(vb, kend, vecb);
         }
         const float* sa = smem + 2 * cur * SLAB;
         const float* sb = sa + SLAB;
@@ -170,12 +170,12 @@ __device__ __forceinline__ void tr_store4(float* p, const float (&v)[4], int n, 
 
 struct TrSimtParams {
     const float *x, *wg, *wu, *wd, *dy;
-    float *h, *dg, *du;    // [rows, F]
+    float *h, *dg, *du;    // [rows, ldf]
     float* out;                // Y or dX, [rows, C]
     float* part;           // [splits][3][F * C] partial weight gradients
-    int rows, C, F;
+    int rows, C, F, ldf;   // ldf: F up to 4
     int splits, split_rows;
-    int vec;               // float4 accesses allowed
+    bool vc, vd, vo;       // float4 accesses allowed: x, dy, wg and wu; wd; out
     int first;             // the first chunk of rows: the partial sums start here
     int dw_mask;           // which weight gradients (bit 0 dWg, 1 dWu, 2 dWd)
 };
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_gate_kernel(const T
     B.p[1] = p.wu + (long long)f0 * p.C;
     B.lim[0] = B.lim[1] = min(64, p.F - f0);
     float2 acc[8][4] = {};
-    tr_tile<true, true, 2>(acc, A, B, 0, p.C, p.vec, tr_smem);
+    tr_tile<true, true, 2>(acc, A, B, 0, p.C, p.vc, p.vc, tr_smem);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int m = m0 + tr_row(i), f = f0 + tr_col(0, 0);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_gate_kernel(const T
         float h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = tr_act<ACT>(g[e]) * u[e];
-        tr_store4(p.h + (long long)m * p.F + f, h, p.F - f, p.vec);
+        tr_store4(p.h + (long long)m * p.ldf + f, h, p.ldf - f, true);
     }
 }
 
@@ -215,12 +215,12 @@ __global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_out_kernel(const Tr
     float2 acc[8][2 * COLS] = {};
     const int c_end = min(p.C, c0 + 64 * COLS);
     if constexpr (BWD) {
-        tr_tile<true, false, COLS>(acc, tr_rows(p.dg, p.F, p.F, m0, p.rows), tr_rows(p.wg, 1, p.C, c0, c_end), 0, p.F, p.vec,
+        tr_tile<true, false, COLS>(acc, tr_rows(p.dg, p.ldf, p.ldf, m0, p.rows), tr_rows(p.wg, 1, p.C, c0, c_end), 0, p.F, true, p.vc,
                                    tr_smem);
-        tr_tile<true, false, COLS>(acc, tr_rows(p.du, p.F, p.F, m0, p.rows), tr_rows(p.wu, 1, p.C, c0, c_end), 0, p.F, p.vec,
+        tr_tile<true, false, COLS>(acc, tr_rows(p.du, p.ldf, p.ldf, m0, p.rows), tr_rows(p.wu, 1, p.C, c0, c_end), 0, p.F, true, p.vc,
                                    tr_smem);
     } else {
-        tr_tile<true, true, COLS>(acc, tr_rows(p.h, p.F, p.F, m0, p.rows), tr_rows(p.wd, p.F, p.F, c0, c_end), 0, p.F, p.vec,
+        tr_tile<true, true, COLS>(acc, tr_rows(p.h, p.ldf, p.ldf, m0, p.rows), tr_rows(p.wd, p.F, p.F, c0, c_end), 0, p.F, true, p.vd,
                                   tr_smem);
     }
 #pragma unroll
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_out_kernel(const Tr
         for (int g = 0; g < COLS; ++g) {
             const int c = c0 + tr_col(g, 0);
             const float v[4] = {acc[i][2 * g].x, acc[i][2 * g].y, acc[i][2 * g + 1].x, acc[i][2 * g + 1].y};
-            tr_store4(p.out + (long long)m * p.C + c, v, p.C - c, p.vec);
+            tr_store4(p.out + (long long)m * p.C + c, v, p.C - c, p.vo);
         }
     }
 }
@@ -248,11 +248,11 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_grad_kernel(const TrSi
     B.p[1] = p.wu + (long long)f0 * p.C;
     B.lim[0] = B.lim[1] = min(64, p.F - f0);
     float2 acc[8][4] = {};
-    tr_tile<true, true, 2>(acc, tr_rows(p.x, p.C, p.C, m0, p.rows), B, 0, p.C, p.vec, tr_smem);
+    tr_tile<true, true, 2>(acc, tr_rows(p.x, p.C, p.C, m0, p.rows), B, 0, p.C, p.vc, p.vc, tr_smem);
     float2 dh[8][2] = {};
     TrOperand D = tr_rows(p.wd, 1, p.F, f0, p.F);
     D.lim[1] = 0;
-    tr_tile<true, false, 1>(dh, tr_rows(p.dy, p.C, p.C, m0, p.rows), D, 0, p.C, p.vec, tr_smem);
+    tr_tile<true, false, 1>(dh, tr_rows(p.dy, p.C, p.C, m0, p.rows), D, 0, p.C, p.vc, p.vd, tr_smem);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int m = m0 + tr_row(i), f = f0 + tr_col(0, 0);
@@ -269,10 +269,10 @@ __global__ void __launch_bounds__(kTrThreads) evo_tr_simt_grad_kernel(const TrSi
             dg[e] = u[e] * da * d[e];  // (d u may overflow where act' is 0)
             du[e] = d[e] * a;
         }
-        const long long at = (long long)m * p.F + f;
-        tr_store4(p.h + at, h, p.F - f, p.vec);
-        tr_store4(p.dg + at, dg, p.F - f, p.vec);
-        tr_store4(p.du + at, du, p.F - f, p.vec);
+        const long long at = (long long)m * p.ldf + f;
+        tr_store4(p.h + at, h, p.ldf - f, true);
+        tr_store4(p.dg + at, dg, p.ldf - f, true);
+        tr_store4(p.du + at, du, p.ldf - f, true);
     }
 }
 
@@ -290,7 +290,8 @@ static __global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_dw_kernel(co
     const float* a = which == 0 ? p.dg : which == 1 ? p.du : p.dy;
     const float* b = which == 2 ? p.h : p.x;
     float2 acc[8][4] = {};
-    tr_tile<false, false, 2>(acc, tr_rows(a, 1, R, r0, R), tr_rows(b, 1, N, n0, N), m_beg, m_end, p.vec, tr_smem);
+    tr_tile<false, false, 2>(acc, tr_rows(a, 1, which == 2 ? p.C : p.ldf, r0, R), tr_rows(b, 1, which == 2 ? p.ldf : p.C, n0, N),
+                             m_beg, m_end, which != 2 || p.vc, which == 2 || p.vc, tr_smem);
     float* out = p.part + ((long long)split * 3 + which) * p.F * p.C;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -306,7 +307,7 @@ static __global__ void __launch_bounds__(kTrThreads, 2) evo_tr_simt_dw_kernel(co
                 for (int e = 0; e < 4; ++e)
                     if (n + e < N) v[e] += o[e];
             }
-            tr_store4(o, v, N - n, p.vec);
+            tr_store4(o, v, N - n, N % 4 == 0);
         }
     }
 }
@@ -324,6 +325,176 @@ static __global__ void __launch_bounds__(256) evo_tr_dw_reduce_kernel(const floa
         for (int k = 0; k < splits; ++k) s += part[((long long)k * 3 + w) * n + i];
         out[w][i] = s;
     }
+}
+
+// ---------------------------------------------------------- products in parts
+
+// Few row tiles leave most of the SMs without a block, and a block walks all of K, one
+// slab after another.  Then the products are taken in parts: ranges of K with a
+// slot of their own, which a second kernel adds in order (and, for G, U and dH, turns into
+// H, dG and dU), in tiles of 128 or 32 rows.  Which tile and how many ranges:
+// tr_parts in evo_blocks.cu.  Still bound by the tiles' walk over K, now shorter; whole
+// calls with and without parts, us: backward 2 x 752 x 3008 75 / 523, 64 x 384 x 1536 62 / 286, 165 x 656 x
+// 2558 203 / 731; forward 192 x 384 x 1536 41 / 159, 96 x 1024 x 4096 98 / 404, 411 x 602 x 2408 142 / 382
+// (the products by PyTorch and plain operators: 187, 184, 270; 100, 193, 156).
+
+// 32 rows x 128 columns: 4 rows of a warp's own by 4 columns a thread.  acc += A B^T
+// over k in [kbeg, kend).
+template <bool BKC>
+__device__ __forceinline__ void tr_tile32(float2 (&acc)[4][2], const TrOperand& A, const TrOperand& B, int kbeg, int kend,
+                                          bool veca, bool vecb, float* smem) {
+    constexpr int SLAB = kTrK * kTrLd;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const bool mine = threadIdx.x < 64;  // 32 rows x 16 k, 8 k of a row each
+    float va[8], vb[8];
+    TrFetch<true> fa(A, kbeg);
+    TrFetch<BKC> fb(B, kbeg);
+    if (kbeg < kend) {
+        if (mine) fa.load(va, kend, veca);
+        fb.load(vb, kend, vecb);
+        if (mine) tr_put<true>(smem, va);
+        tr_put<BKC>(smem + SLAB, vb);
+    }
+    __syncthreads();
+    int cur = 0;
+    for (int k0 = kbeg; k0 < kend; k0 += kTrK) {
+        const bool more = k0 + kTrK < kend;
+        if (more) {
+            if (mine) fa.load(va, kend, veca);
+            fb.load(vb, kend, vecb);
+        }
+        const float* sa = smem + 2 * cur * SLAB;
+        const float* sb = sa + SLAB;
+#pragma unroll
+        for (int k = 0; k < kTrK; ++k) {
+            const float4 a = *reinterpret_cast<const float4*>(sa + k * kTrLd + 4 * ty);
+            const float4 b = *reinterpret_cast<const float4*>(sb + k * kTrLd + 4 * tx);
+            const float r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 ai = make_float2(r[i], r[i]);
+                tr_fma2(acc[i][0], ai, make_float2(b.x, b.y));
+                tr_fma2(acc[i][1], ai, make_float2(b.z, b.w));
+            }
+        }
+        if (more) {
+            cur ^= 1;
+            if (mine) tr_put<true>(smem + 2 * cur * SLAB, va);
+            tr_put<BKC>(smem + 2 * cur * SLAB + SLAB, vb);
+            __syncthreads();
+        }
+    }
+}
+
+// out = A B^T, A [rows, K] with k contiguous; B [N, K] with k contiguous (kc), else [K, N].
+struct TrJob {
+    const float *a, *b;
+    int lda;
+    bool kc, veca, vecb;
+};
+enum TrLayoutOfB { TR_B_K, TR_B_N, TR_B_MIXED };  // contiguous along k in every job, in none, in some
+
+struct TrPartParams {
+    TrJob job[3];
+    int jobs, splits;
+    int rows, N, K;
+    int ld;             // of a slot's rows: N up to 4
+    float* slots;       // [splits][jobs][rows][ld]
+};
+
+// ROWS x 64 * COLS (128 columns with 32 rows) of one job over one range of K a block.
+template <int ROWS, int COLS, int B_LAYOUT>
+__global__ void __launch_bounds__(kTrThreads, ROWS == 32 ? 4 : 2) evo_tr_simt_part_kernel(const __grid_constant__ TrPartParams p) {
+    extern __shared__ __align__(16) float tr_smem[];
+    const int j = blockIdx.z % p.jobs, split = blockIdx.z / p.jobs;
+    const int n0 = blockIdx.x * 64 * COLS, m0 = blockIdx.y * ROWS;
+    const int per = ((p.K + kTrK - 1) / kTrK + p.splits - 1) / p.splits * kTrK;
+    const int kbeg = split * per, kend = min(p.K, kbeg + per);
+    const bool kc = B_LAYOUT == TR_B_K || (B_LAYOUT == TR_B_MIXED && p.job[j].kc);
+    const bool veca = p.job[j].veca, vecb = p.job[j].vecb;
+    const TrOperand A = tr_rows(p.job[j].a, p.job[j].lda, p.job[j].lda, m0, min(p.rows, m0 + ROWS));
+    const TrOperand B = tr_rows(p.job[j].b, kc ? p.K : 1, kc ? p.K : p.N, n0, min(p.N, n0 + 64 * COLS));
+    float* out = p.slots + (long long)blockIdx.z * p.rows * p.ld;
+    if constexpr (ROWS == 32) {
+        float2 acc[4][2] = {};
+        if (kc) tr_tile32<true>(acc, A, B, kbeg, kend, veca, vecb, tr_smem);
+        else tr_tile32<false>(acc, A, B, kbeg, kend, veca, vecb, tr_smem);
+        const int n = n0 + 4 * int(threadIdx.x & 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = m0 + 4 * int(threadIdx.x >> 5) + i;
+            const float v[4] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y};
+            if (m < p.rows) tr_store4(out + (long long)m * p.ld + n, v, p.ld - n, true);
+        }
+    } else {
+        float2 acc[8][2 * COLS] = {};
+        if (kc) tr_tile<true, true, COLS>(acc, A, B, kbeg, kend, veca, vecb, tr_smem);
+        else tr_tile<true, false, COLS>(acc, A, B, kbeg, kend, veca, vecb, tr_smem);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int m = m0 + tr_row(i);
+            if (m >= p.rows) continue;
+#pragma unroll
+            for (int g = 0; g < COLS; ++g) {
+                const int n = n0 + tr_col(g, 0);
+                const float v[4] = {acc[i][2 * g].x, acc[i][2 * g].y, acc[i][2 * g + 1].x, acc[i][2 * g + 1].y};
+                tr_store4(out + (long long)m * p.ld + n, v, p.ld - n, true);
+            }
+        }
+    }
+}
+
+// four elements at `at` of slots `first`, `first + step`, .., added in order
+__device__ __forceinline__ float4 tr_slots(const float* slots, long long slot, int first, int step, int count, long long at) {
+    float4 s = *reinterpret_cast<const float4*>(slots + first * slot + at);
+    for (int k = 1; k < count; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(slots + (first + (long long)k * step) * slot + at);
+        s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
+    }
+    return s;
+}
+
+// H (and dG, dU) of four features a thread from the slots of G, U (and dH).
+template <int ACT, bool BWD>
+__global__ void __launch_bounds__(256) evo_tr_join_act_kernel(const float* slots, int splits, int rows, int ld,
+                                                              float* h, float* dg, float* du) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, slot = (long long)rows * ld;
+    if (4 * i >= slot) return;
+    constexpr int jobs = BWD ? 3 : 2;
+    const float4 gs = tr_slots(slots, slot, 0, jobs, splits, 4 * i), us = tr_slots(slots, slot, 1, jobs, splits, 4 * i);
+    const float g[4] = {gs.x, gs.y, gs.z, gs.w}, u[4] = {us.x, us.y, us.z, us.w};
+    const long long at = 4 * i;  // H's rows are as long as the slots'
+    float hv[4];
+    if constexpr (BWD) {
+        const float4 ds = tr_slots(slots, slot, 2, jobs, splits, 4 * i);
+        const float d[4] = {ds.x, ds.y, ds.z, ds.w};
+        float dgv[4], duv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float a, da;
+            tr_act_grad<ACT>(g[e], a, da);
+            hv[e] = a * u[e];
+            dgv[e] = u[e] * da * d[e];
+            duv[e] = d[e] * a;
+        }
+        *reinterpret_cast<float4*>(dg + at) = make_float4(dgv[0], dgv[1], dgv[2], dgv[3]);
+        *reinterpret_cast<float4*>(du + at) = make_float4(duv[0], duv[1], duv[2], duv[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hv[e] = tr_act<ACT>(g[e]) * u[e];
+    }
+    *reinterpret_cast<float4*>(h + at) = make_float4(hv[0], hv[1], hv[2], hv[3]);
+}
+
+// Y or dX, four channels a thread, from all of its slots.
+static __global__ void __launch_bounds__(256) evo_tr_join_out_kernel(const float* slots, int count, int rows, int C, int ld,
+                                                                     float* out, int vec) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, slot = (long long)rows * ld;
+    if (4 * i >= slot) return;
+    const int m = int(4 * i / ld), c = int(4 * i - (long long)m * ld);
+    const float4 s = tr_slots(slots, slot, 0, 1, count, 4 * i);
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    tr_store4(out + (long long)m * C + c, v, C - c, vec);
 }
 
 }  // namespace evo
