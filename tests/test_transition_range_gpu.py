@@ -189,3 +189,22 @@ def test_a_sum_past_the_range_is_a_closed_gate(M, C, F, dt, act):
     grads = evo.transition_backward(x, wg, wu, wd, torch.ones_like(x), act=act)
     assert evo.evo_attn_sync_status() == evo.EVO_OK
     assert all((t == 0).all() for t in (y, *grads))
+
+
+@pytest.mark.parametrize("M,C,F,dt", [(70, 16, 16, BF16), (70, 136, 24, BF16), (70, 300, 100, BF16), (1, 16, 16, BF16),
+                                      (70, 16, 16, FP32), (7000, 136, 24, FP32)], ids=str)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_a_sum_past_the_range_is_an_open_gate(M, C, F, dt, act):
+    """G = 6e38: act is infinite however small U is, and its slope is 1."""
+    x, wg, wu, wd = inputs(torch.tensor([[2.0, 0.5]] * M), C, F, dt)
+    x[:, 2] = 2.0
+    wg[0, 0], wg[0, 2], wg[1:] = 1.5e38, 1.5e38, 0.0
+    y = evo.transition(x, wg, wu, wd, act=act)
+    dy = torch.zeros_like(x)
+    dy[:, 0] = 0.25
+    _, dwg, _, _ = evo.transition_backward(x, wg, wu, wd, dy, act=act)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    assert (y[:, 0] == float("inf")).all()
+    # dWg[0, 0] = sum of dH U X = 0.25 * 0.5 * 2, exact in fp32 up to 2^22 rows
+    want = torch.tensor(0.25 * M).to(dt)
+    assert float(dwg[0, 0]) == float(want) and float(dwg[0, 2]) == float(want)

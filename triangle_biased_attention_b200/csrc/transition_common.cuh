@@ -28,33 +28,36 @@ __device__ __forceinline__ float tr_sigmoid(float g) {
     return __fdividef(g < 0.0f ? e : 1.0f, 1.0f + e);
 }
 
-// A gate as a factor of its sigmoid or Phi: finite, so that a sum G that has
-// overflowed gives act's limits, 0 and (times a factor or rounded) infinity, and not 0
-// times infinity.  NaN stays.
+// A gate as a factor of its sigmoid or Phi: above -infinity, so that a sum G that has
+// overflowed gives act's limit 0 and not 0 times infinity.  NaN stays.
+__device__ __forceinline__ float tr_above(float g) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-3.402823466e38f));
+    return g;
+}
+// The same on both sides, for the term of act' that vanishes on both.
 __device__ __forceinline__ float tr_finite(float g) {
-    const float big = 3.402823466e38f;
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(big));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-big));
+    g = tr_above(g);
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(3.402823466e38f));
     return g;
 }
 
-// act(g) and its derivative.  silu: g s, s (1 + g (1 - s)) with s = sigmoid(g);
+// act(g) and its derivative.  silu: g s, s + g s (1 - s) with s = sigmoid(g);
 // gelu: g Phi(g), Phi(g) + g phi(g), Phi and phi the normal distribution and density.
 template <int ACT>
 __device__ __forceinline__ float tr_act(float g) {
-    if constexpr (ACT == EVO_ACT_SILU) return tr_finite(g) * tr_sigmoid(g);
-    else return tr_finite(g) * (0.5f * erfcf(-0.70710678118654752f * g));
+    if constexpr (ACT == EVO_ACT_SILU) return tr_above(g) * tr_sigmoid(g);
+    else return tr_above(g) * (0.5f * erfcf(-0.70710678118654752f * g));
 }
 
 template <int ACT>
 __device__ __forceinline__ void tr_act_grad(float g, float& a, float& da) {
     if constexpr (ACT == EVO_ACT_SILU) {
         const float s = tr_sigmoid(g);
-        a = tr_finite(g) * s;
-        da = fmaf(a, 1.0f - s, s);
+        a = tr_above(g) * s;
+        da = fmaf(tr_finite(g) * s, 1.0f - s, s);
     } else {
         const float phi = 0.5f * erfcf(-0.70710678118654752f * g);
-        a = tr_finite(g) * phi;
+        a = tr_above(g) * phi;
         da = fmaf(tr_finite(g) * 0.3989422804014327f, expf(-0.5f * g * g), phi);
     }
 }

@@ -158,6 +158,7 @@ __device__ __forceinline__ bool tr_near(const float (&g)[N]) {
     return m[0] <= kTrNear;
 }
 
+__device__ __forceinline__ float2 tr_above2(float2 g) { return make_float2(tr_above(g.x), tr_above(g.y)); }
 __device__ __forceinline__ float2 tr_finite2(float2 g) { return make_float2(tr_finite(g.x), tr_finite(g.y)); }
 
 // Phi(-|g|) e^(g^2/2) = t (c0 + c1 t + .. + c6 t^6), t = 1 / (1 + kPhiT |g|): fitted for the
@@ -202,7 +203,7 @@ __device__ __forceinline__ float2 tr_gate2(float2 g, float2 u) {
     float2 p, e;
     if constexpr (ACT == EVO_ACT_SILU) p = tr_sigmoid2<FAR>(g);
     else p = tr_phi2<FAR>(g, e);
-    return tr_mul2(tr_mul2(FAR ? tr_finite2(g) : g, p), u);
+    return tr_mul2(tr_mul2(FAR ? tr_above2(g) : g, p), u);
 }
 
 // h, dg and du of a pair from g, u and d = dH
@@ -211,9 +212,9 @@ __device__ __forceinline__ void tr_grad2(float2 g, float2 u, float2 d, float2& h
     float2 p, e, da;
     if constexpr (ACT == EVO_ACT_SILU) p = tr_sigmoid2<FAR>(g);
     else p = tr_phi2<FAR>(g, e);
+    const float2 a = tr_mul2(FAR ? tr_above2(g) : g, p);
     if (FAR) g = tr_finite2(g);
-    const float2 a = tr_mul2(g, p);
-    if constexpr (ACT == EVO_ACT_SILU) da = tr_mad2(a, tr_mad2(p, tr_both(-1.0f), tr_both(1.0f)), p);
+    if constexpr (ACT == EVO_ACT_SILU) da = tr_mad2(FAR ? tr_mul2(g, p) : a, tr_mad2(p, tr_both(-1.0f), tr_both(1.0f)), p);
     else da = tr_mad2(tr_mul2(g, tr_both(0.3989422804014327f)), e, p);
     h = tr_mul2(a, u);
     du = tr_mul2(d, a);
