@@ -125,7 +125,7 @@ TrPart tr_parts(int64_t rows, int64_t N, int64_t K, int64_t jobs, bool odd, doub
     TrPart best;
     double least = 0.95 * whole;  // (what an estimate may be off by is not worth two launches)
     for (const TrTile& t : kTrTiles)
-        for (int splits = 1; splits <= 64; ++splits) {
+        for (int splits = 1; splits <= 64; splits += std::max(1, splits / 4)) {
             const int64_t slabs = (K + splits * evo::kTrK - 1) / (splits * evo::kTrK);
             const double bytes = 4.0 * double(rows) * double(N) * double(jobs) * splits;  // of the slots
             if ((splits > 1 && slabs < 2) || bytes > 128e6 || (rows + t.rows - 1) / t.rows > 65535) break;
@@ -144,7 +144,7 @@ TrPart tr_parts(int64_t rows, int64_t N, int64_t K, int64_t jobs, bool odd, doub
 int64_t tr_dw_splits(int64_t rows, int64_t C, int64_t F) {
     int64_t best = 1;
     double least = 0;
-    for (int64_t splits = 1; splits <= 128; ++splits) {
+    for (int64_t splits = 1; splits <= 148; splits += std::max<int64_t>(1, splits / 8)) {
         const int64_t per = (rows + splits - 1) / splits;
         if (splits > 1 && per < 4 * evo::kTrK) break;
         const double time = tr_walk(kTrDw, 3 * tr_tiles(kTrDw, F, C) * splits, per, C % 4 != 0) + double(splits) * 24.0 * double(C) * double(F) / 4e6;
@@ -381,10 +381,8 @@ bool run_out_parts(const TrPart& t, const evo::TrSimtParams& p, float* slots, cu
 }
 
 template <int ACT>
-int run_fwd_simt(const float* X, const float* Wg, const float* Wu, const float* Wd, float* Y, char* ws, int64_t M, int64_t C, int64_t F,
-                 int dtype, cudaStream_t st) {
-    TrLayout L;
-    tr_layout(M, C, F, dtype, false, &L);  // checked by the caller
+int run_fwd_simt(const TrLayout& L, const float* X, const float* Wg, const float* Wu, const float* Wd, float* Y, char* ws, int64_t M,
+                 int64_t C, int64_t F, cudaStream_t st) {
     evo::TrSimtParams p = {};
     p.wg = Wg;
     p.wu = Wu;
@@ -411,10 +409,8 @@ int run_fwd_simt(const float* X, const float* Wg, const float* Wu, const float* 
 }
 
 template <int ACT>
-int run_bwd_simt(const float* X, const float* Wg, const float* Wu, const float* Wd, const float* dY, float* dX, float* dWg, float* dWu, float* dWd,
-                 char* ws, int64_t M, int64_t C, int64_t F, int dtype, cudaStream_t st) {
-    TrLayout L;
-    tr_layout(M, C, F, dtype, true, &L);
+int run_bwd_simt(const TrLayout& L, const float* X, const float* Wg, const float* Wu, const float* Wd, const float* dY, float* dX,
+                 float* dWg, float* dWu, float* dWd, char* ws, int64_t M, int64_t C, int64_t F, cudaStream_t st) {
     evo::TrSimtParams p = {};
     p.wg = Wg;
     p.wu = Wu;
@@ -890,7 +886,7 @@ extern "C" EVO_API int evo_transition_fwd(const void* X, const void* Wg, const v
     if (dtype == EVO_DTYPE_FP32) {
         auto f = [](const void* p) { return static_cast<const float*>(p); };
         auto run = act == EVO_ACT_SILU ? run_fwd_simt<EVO_ACT_SILU> : run_fwd_simt<EVO_ACT_GELU>;
-        return run(f(X), f(Wg), f(Wu), f(Wd), static_cast<float*>(Y), ws, M, C, F, dtype, st);
+        return run(L, f(X), f(Wg), f(Wu), f(Wd), static_cast<float*>(Y), ws, M, C, F, st);
     }
     auto run = dtype == EVO_DTYPE_FP16
                    ? (act == EVO_ACT_SILU ? run_fwd_mma<true, EVO_ACT_SILU> : run_fwd_mma<true, EVO_ACT_GELU>)
@@ -941,7 +937,7 @@ extern "C" EVO_API int evo_transition_bwd(const void* X, const void* Wg, const v
         auto f = [](const void* p) { return static_cast<const float*>(p); };
         auto o = [](void* p) { return static_cast<float*>(p); };
         auto run = act == EVO_ACT_SILU ? run_bwd_simt<EVO_ACT_SILU> : run_bwd_simt<EVO_ACT_GELU>;
-        return run(f(X), f(Wg), f(Wu), f(Wd), f(dY), o(dX), o(dWg), o(dWu), o(dWd), ws, M, C, F, dtype, st);
+        return run(L, f(X), f(Wg), f(Wu), f(Wd), f(dY), o(dX), o(dWg), o(dWu), o(dWd), ws, M, C, F, st);
     }
     auto run = dtype == EVO_DTYPE_FP16
                    ? (act == EVO_ACT_SILU ? run_bwd_mma<true, EVO_ACT_SILU> : run_bwd_mma<true, EVO_ACT_GELU>)
