@@ -539,7 +539,9 @@ def transition(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down
     dtype.  act: "silu" or "gelu" (erf form).  ``workspace``: optional uint8 CUDA
     tensor of ``evo_transition_fwd_workspace_size`` bytes (allocated here when
     not given; calls that may run at the same time need one each).  Runs on
-    ``stream`` (default: the current stream) without synchronising.
+    ``stream`` (default: the current stream) without synchronising.  Like the
+    attention it records nothing for autograd: the result does not require grad,
+    whatever the inputs do (``transition_backward`` gives the gradients).
     """
     M, C, F = _transition_args(x, w_gate, w_up, w_down, act)
     on = _OnStream(stream, x.device)
@@ -657,7 +659,8 @@ def relpos_bias(table: torch.Tensor, borders: torch.Tensor, pos: torch.Tensor, p
     [B, Sk], default pos.  chain, chain_k: int32 like pos and pos_k, or None.
     base: optional bias [B, 1, H, Sq, Sk] added to it.  All contiguous on one
     CUDA device.  Runs on ``stream`` (default: the current stream) without
-    synchronising.
+    synchronising.  Records nothing for autograd (``relpos_bias_backward`` gives
+    the table's gradient).
     """
     if table.dim() != 2:
         raise ValueError("table must be [R, H]")

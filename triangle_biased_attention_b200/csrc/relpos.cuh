@@ -145,8 +145,8 @@ __device__ __forceinline__ uint32_t rel_add(uint32_t a, uint32_t b) {
 // its columns lie the block's width apart and are written one by one.
 // 2048 x 2048 x 8 heads, bf16, with a base: 30.9 us, 134 MB, 4.35 TB/s (L2 takes part of
 // the writes); one shared-memory read for all heads instead of one each, and 16-byte
-// writes, brought it from 254 us.  The loads and stores in flight are the limit
-// now (issue 39 %).
+// writes, brought it from 254 us.  Its 683 blocks of 3 rows take 2.3 rounds, each with
+// the tables to fill first (issue 39 %).
 template <typename T, int NW, bool VEC>
 __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const RelParams<T> p) {
     constexpr int HEADS = NW * 4 / int(sizeof(T));
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kRelThreads, 2) evo_relpos_fwd_kernel(const Re
 // another range of bins: the one behind the last, which nobody reads) and the
 // positions are kept as byte offsets into it: an element costs a subtraction, a
 // clamp, a read and an addition.  1733 x 1733 x 16 heads, fp32: 67.6 us, 192 MB, 2.84 TB/s, the
-// issue slots 67 % busy (an odd row length allows 4-byte loads only, and log-spaced
+// issue slots 66 % busy (an odd row length allows 4-byte loads only, and log-spaced
 // buckets move some column of a warp in most rows).  That needs positions below 2^27 in size and
 // borders within the table's span; other blocks search the borders.
 // VEC: a thread's columns are runs of 16 whole bytes; else they lie the block's

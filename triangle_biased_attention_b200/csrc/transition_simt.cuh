@@ -7,9 +7,10 @@
 // conflict-free.  K advances in slabs of 16, double-buffered: the next slab's
 // global loads are in flight while the current one is multiplied.  The products
 // use the packed two-lane FMA, which halves the FMA instructions issued.
-// Bound by the FMA pipes: 16384 rows, C = 128, F = 512: 176 us forward, 36.6 TFLOP/s, half
+// Bound by the FMA pipes: 16384 rows, C = 128, F = 512: 175 us forward, 36.8 TFLOP/s, half
 // of the pipes' 74 TFLOP/s at the highest clock; what is lost is the issue slots
-// of the shared-memory reads and of the slabs' stores.  Two blocks an SM measured
+// of the shared-memory reads and of the slabs' stores, and the gate kernel's spills
+// (288 bytes stored, 152 loaded a thread).  Two blocks an SM measured
 // 177 us against 182 for one, plain FMAs 187 us.
 // The B operand is two groups of 64 rows with pointers of their own: the gate
 // and the up projection of the same 64 features come out in the same thread, so

@@ -651,8 +651,8 @@ evo_tr_mma_kernel(const __grid_constant__ TrMaps maps, const TrMmaParams p) {
 // 2000 cycles of a tile's 12000 at C = 128).
 //
 // 131072 rows, C = 256, F = 1024: 163 us, 1.27 PFLOP/s, the tensor pipe 80 % busy at the
-// 1.5 GHz that the power limit leaves.  589824 rows, C = 128, F = 512: 230 us, 1.0
-// PFLOP/s: tensor pipe and special functions 60 % busy each, because a chunk's G and
+// 1.5 GHz that the power limit leaves.  589824 rows, C = 128, F = 512: 229 us, 1.0
+// PFLOP/s: tensor pipe and special functions 63 % busy each, because a chunk's G and
 // U have one place in tensor memory and the activation and GU wait for each other.
 // (64-feature chunks in two places, two groups of warps in turn: 248 us; an N = 128
 // MMA keeps its issuer as busy as an N = 256 one.)
