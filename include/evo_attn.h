@@ -467,8 +467,9 @@ EVO_API int64_t evo_relpos_bwd_workspace_size(int64_t B, int64_t Sq, int64_t Sk,
  *   workspace  device scratch of at least evo_relpos_bwd_workspace_size bytes,
  *              256-byte aligned, owned by the caller, overwritten.
  *
- * Sums are held in fp32 in a fixed order (no atomics): the same call gives the
- * same bits every time.  Also needs B * H * ceil(R / 256) <= 65535.  dtable and
+ * Sums are held in fp32, less than 4096 additions deep, and across tiles of query
+ * rows in fp64, in a fixed order (no atomics): the same call gives the same bits
+ * every time.  Also needs B * H * ceil(R / 256) <= 65535.  dtable and
  * the workspace must not overlap each other or any input.
  */
 EVO_API int evo_relpos_bwd(const void* dpair, const int32_t* borders, const int32_t* pos_q, const int32_t* pos_k,

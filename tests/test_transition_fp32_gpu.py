@@ -78,3 +78,21 @@ def test_unaligned_same_bits_streams_and_graph(M, C, F):
     out = torch.full((M + 3, C), 5.0, device="cuda")
     evo.transition(*args[:4], out=out[:M])
     assert torch.equal(out[:M], want[0]) and (out[M:] == 5).all()
+
+
+@pytest.mark.parametrize("M,C,F", [(3, 64, 96), (124, 100, 400), (20, 256, 1024), (7000, 128, 64)])
+def test_outputs_that_are_not_16_byte_aligned(M, C, F):
+    def hole(*shape):
+        return torch.full((int(np.prod(shape)) + 5,), 7.0, device="cuda")[1:]
+    x, wg, wu, wd, dy = args = make(M, C, F, FP32, seed=5)
+    want = [evo.transition(*args[:4]), *evo.transition_backward(*args)]
+    buf = hole(M, C)
+    assert torch.equal(evo.transition(*args[:4], out=buf[:M * C].view(M, C)), want[0]) and (buf[M * C:] == 7).all()
+    bufs = [hole(*t.shape) for t in want[1:]]
+    ws = torch.empty(evo.evo_transition_bwd_workspace_size(M, C, F, evo.EVO_DTYPE_FP32), dtype=torch.uint8, device="cuda")
+    st = evo.evo_transition_bwd(*(t.data_ptr() for t in args), *(b.data_ptr() for b in bufs), ws.data_ptr(), ws.numel(), M, C,
+                                F, evo.EVO_ACT_SILU, evo.EVO_DTYPE_FP32, None)
+    torch.cuda.synchronize()
+    assert st == evo.EVO_OK
+    for b, t in zip(bufs, want[1:]):
+        assert torch.equal(b[:t.numel()].view(t.shape), t) and (b[t.numel():] == 7).all()

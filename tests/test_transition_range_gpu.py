@@ -208,3 +208,29 @@ def test_a_sum_past_the_range_is_an_open_gate(M, C, F, dt, act):
     # dWg[0, 0] = sum of dH U X = 0.25 * 0.5 * 2, exact in fp32 up to 2^22 rows
     want = torch.tensor(0.25 * M).to(dt)
     assert float(dwg[0, 0]) == float(want) and float(dwg[0, 2]) == float(want)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,C,F,dt", [(70, 64, 96, BF16), (300, 136, 200, FP16), (65, 50, 70, BF16), (70, 64, 96, FP32),
+                                      (5000, 64, 96, FP32)], ids=str)
+def test_nan_stays_in_its_row_and_its_feature(M, C, F, dt, act):
+    gen = torch.Generator().manual_seed(M)
+    x, wg, wu, wd, dy = ((torch.randn(*s, generator=gen) * k).to(dt).cuda() for s, k in
+                         (((M, C), 1), ((F, C), C ** -0.5), ((F, C), C ** -0.5), ((C, F), F ** -0.5), ((M, C), 1)))
+    clean = evo.transition_backward(x, wg, wu, wd, dy, act=act)
+    bad = x.clone()
+    bad[M // 2, 3] = float("nan")
+    dx, *dw = evo.transition_backward(bad, wg, wu, wd, dy, act=act)
+    rest = torch.arange(M) != M // 2
+    assert torch.isnan(dx[M // 2]).all() and torch.equal(dx[rest], clean[0][rest])
+    assert all(torch.isnan(w).all() for w in dw)
+    # a gate weight: its own feature's rows and column of the gradients, none beside it
+    bad = wg.clone()
+    bad[33, 2] = float("nan")
+    assert torch.isnan(evo.transition(x, bad, wu, wd, act=act)).all()
+    dx, *dw = evo.transition_backward(x, bad, wu, wd, dy, act=act)
+    assert evo.evo_attn_sync_status() == evo.EVO_OK
+    rest = torch.arange(F) != 33
+    assert torch.isnan(dx).all()
+    for w in (dw[0], dw[1], dw[2].T):
+        assert torch.isnan(w[33]).all() and torch.isfinite(w[rest]).all()

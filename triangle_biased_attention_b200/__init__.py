@@ -692,7 +692,8 @@ def relpos_bias_backward(dpair: torch.Tensor, borders: torch.Tensor, pos: torch.
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The gradient [R, H] of ``relpos_bias``'s table for the gradient dpair
     ([B, 1, H, Sq, Sk], as ``evo_attn_backward`` returns it) of its result; the
-    gradient of ``base`` is dpair itself.  ``workspace``: optional uint8 CUDA tensor of
+    gradient of ``base`` is dpair itself.  Needs B * H * ceil(R / 256) <= 65535.
+    ``workspace``: optional uint8 CUDA tensor of
     ``evo_relpos_bwd_workspace_size`` bytes.  Runs on ``stream`` (default: the
     current stream) without synchronising."""
     if dpair.dim() != 5:

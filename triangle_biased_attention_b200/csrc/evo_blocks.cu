@@ -155,7 +155,7 @@ int64_t tr_dw_splits(int64_t rows, int64_t C, int64_t F) {
 
 struct TrLayout {
     int64_t chunk = 0;                            // rows of a chunk
-    int64_t h = 0, dg = 0, du = 0;                // [chunk, F] (16-bit: rows up to 128, F up to 128)
+    int64_t h = 0, dg = 0, du = 0;                // [chunk, F] (16-bit: rows up to 128, F up to 128; fp32: F up to 4)
     int64_t part = 0, part2 = 0, part3 = 0;       // partial weight gradients, fp32: [splits][R][N up to 4] (fp32 call: one)
     bool direct = false;                          // 16-bit: the last products are the weight gradients
     int64_t splits = 0, split_rows = 0;           // ranges of rows with a slot of their own
